@@ -86,7 +86,7 @@ def draw(rng):
         T = R * _log(rng, 1, max(1, min(16384, 65536 * 2048 // (k * I)) // R))
         return dict(case, T=T, I=I, out=out) if op == "swiglu" else dict(case, T=T, I=I)
     form = rng.choice(["bf16", "fp8", "mxfp4"]) if op == "product" else "bf16"
-    K, N = _log(rng, 128, 7168, {"bf16": 8, "fp8": 128, "mxfp4": 32}[form]), _log(rng, 64, 7168, 8)
+    K, N = _log(rng, 128, 7168, 8 if form == "bf16" else 128), _log(rng, 64, 7168, 8)
     if op == "gradient":  # the weight gradient is as large as the weights
         K, N = (K, N) if E * K * N <= 5e8 else (_log(rng, 128, 2048, 8), _log(rng, 64, 2048, 8))
     most = max(1, int(min(16384, 1.5e12 / (2.0 * K * N * k))) // R)
