@@ -29,6 +29,10 @@ EP_ST_CAPACITY = 4
 EP_ST_TIMEOUT = 8
 EP_ST_BAD_HANDLE = 16
 
+EP_FORM_BF16 = 0
+EP_FORM_FP8 = 1
+EP_FORM_MXFP4 = 2
+
 c_void_p = ctypes.c_void_p
 
 
@@ -61,6 +65,14 @@ SIZE_FIELDS = ("cnt_se", "cnt_sd", "recv_cnt", "expert_off", "rank_rows", "src_e
 class EpSizes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in SIZE_FIELDS]
 
+
+class EpGroups(ctypes.Structure):
+    _fields_ = [("offsets", c_void_p), ("counts", c_void_p), ("num_experts", ctypes.c_int32),
+                ("num_ranks", ctypes.c_int32), ("cap_rows", ctypes.c_int64), ("region_rows", ctypes.c_int64),
+                ("rows_hint", ctypes.c_int64)]
+
+
+_GROUPS = ctypes.POINTER(EpGroups)
 
 # (name, restype, argtypes) for every symbol include/ep.h declares
 SIGNATURES = {
@@ -113,6 +125,20 @@ SIGNATURES = {
                                        ctypes.c_int64, c_void_p]),
     "ep_pattern_gather": (ctypes.c_int, [c_void_p, c_void_p, c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_int64, ctypes.c_int, c_void_p]),
+    "ep_expert_gemm": (ctypes.c_int, [_GROUPS, ctypes.c_int, c_void_p, c_void_p, c_void_p, c_void_p, ctypes.c_int,
+                                      ctypes.c_int, c_void_p, c_void_p]),
+    "ep_expert_gemm_dgrad": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int, ctypes.c_int, c_void_p,
+                                            c_void_p]),
+    "ep_expert_gemm_wgrad": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int, ctypes.c_int, c_void_p,
+                                            ctypes.c_int, ctypes.c_int, c_void_p]),
+    "ep_swiglu": (ctypes.c_int, [_GROUPS, c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, c_void_p, c_void_p,
+                                 c_void_p]),
+    "ep_swiglu_backward": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p,
+                                          c_void_p]),
+    "ep_quantize_mxfp4": (ctypes.c_int, [_GROUPS, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p, c_void_p,
+                                         c_void_p]),
+    "ep_dequantize_mxfp4": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p,
+                                           c_void_p]),
 }
 
 _lib = None
@@ -285,6 +311,49 @@ def ep_pattern_gather(rows: int, pos: int, out: int, num_tokens: int, num_topk: 
                       capped: bool, stream: int) -> None:
     _check(load().ep_pattern_gather(rows, pos, out, num_tokens, num_topk, hidden, num_rows, int(capped), stream),
            "ep_pattern_gather")
+
+
+def _ref(groups: Optional[EpGroups]):
+    return None if groups is None else ctypes.byref(groups)
+
+
+def ep_expert_gemm(groups: EpGroups, form: int, rows: int, row_scales: Optional[int], weights: int,
+                   weight_scales: Optional[int], K: int, N: int, out: int, stream: int) -> None:
+    _check(load().ep_expert_gemm(_ref(groups), form, rows, row_scales, weights, weight_scales, K, N, out, stream),
+           "ep_expert_gemm")
+
+
+def ep_expert_gemm_dgrad(groups: EpGroups, grad_out: int, weights: int, K: int, N: int, grad_rows: int,
+                         stream: int) -> None:
+    _check(load().ep_expert_gemm_dgrad(_ref(groups), grad_out, weights, K, N, grad_rows, stream),
+           "ep_expert_gemm_dgrad")
+
+
+def ep_expert_gemm_wgrad(groups: EpGroups, grad_out: int, rows: int, K: int, N: int, grad_weights: int, out_f32: bool,
+                         accumulate: bool, stream: int) -> None:
+    _check(load().ep_expert_gemm_wgrad(_ref(groups), grad_out, rows, K, N, grad_weights, int(out_f32), int(accumulate),
+                                       stream), "ep_expert_gemm_wgrad")
+
+
+def ep_swiglu(groups: Optional[EpGroups], gate_up: int, num_rows: int, I: int, form: int, out: int,
+              scales: Optional[int], stream: int) -> None:
+    _check(load().ep_swiglu(_ref(groups), gate_up, num_rows, I, form, out, scales, stream), "ep_swiglu")
+
+
+def ep_swiglu_backward(groups: Optional[EpGroups], grad_out: int, gate_up: int, num_rows: int, I: int,
+                       grad_gate_up: int, stream: int) -> None:
+    _check(load().ep_swiglu_backward(_ref(groups), grad_out, gate_up, num_rows, I, grad_gate_up, stream),
+           "ep_swiglu_backward")
+
+
+def ep_quantize_mxfp4(groups: Optional[EpGroups], x: int, num_rows: int, cols: int, q: int, scales: int,
+                      stream: int) -> None:
+    _check(load().ep_quantize_mxfp4(_ref(groups), x, num_rows, cols, q, scales, stream), "ep_quantize_mxfp4")
+
+
+def ep_dequantize_mxfp4(groups: Optional[EpGroups], q: int, scales: int, num_rows: int, cols: int, x: int,
+                        stream: int) -> None:
+    _check(load().ep_dequantize_mxfp4(_ref(groups), q, scales, num_rows, cols, x, stream), "ep_dequantize_mxfp4")
 
 
 # ---------------------------------------------------------------------------
@@ -592,6 +661,17 @@ class Buffer:
                              _stream())
         return out
 
+    def groups(self, layout: Layout) -> "Groups":
+        """The experts' rows after ``dispatch`` / ``dispatch_with_layout``, for
+        the experts' operators (``expert_gemm`` and those beside it)."""
+        return Groups(layout.recv_cnt, layout.expert_off, num_experts=self.E, num_ranks=self.R,
+                      cap_rows=self.cap_rows, rows_hint=self.T * self.k)
+
+    def groups_low_latency(self, recv_count) -> "Groups":
+        """The experts' rows after ``dispatch_low_latency``."""
+        return Groups(recv_count, None, num_experts=self.E, num_ranks=self.R, cap_rows=self.cap_rows,
+                      region_rows=self.T // self.R, rows_hint=self.T * self.k)
+
     def set_num_cus(self, num_cus: int) -> None:
         """The compute units the stream these calls run on may use (0 = all);
         see CuStream."""
@@ -604,6 +684,205 @@ class Buffer:
     def status(self) -> int:
         """Synchronize the current stream; return and clear the sticky status bits."""
         return ep_get_status(self.ctx, _stream())
+
+
+@dataclass
+class Groups:
+    """Which receive rows are whose, for the experts' operators below
+    (ep_groups in include/ep.h): the packed layout of ``dispatch`` (``offsets``
+    and ``counts`` [E] int32 on the device) or, with ``region_rows`` = T/R, the
+    regions of ``dispatch_low_latency`` (``counts`` [E, R], ``offsets`` None).
+    ``Buffer.groups`` and ``Buffer.groups_low_latency`` make them."""
+    counts: "torch.Tensor"
+    offsets: Optional["torch.Tensor"]
+    num_experts: int
+    num_ranks: int
+    cap_rows: int
+    region_rows: int = 0
+    rows_hint: int = 0
+
+    @property
+    def num_rows(self) -> int:
+        return self.num_ranks * self.cap_rows
+
+    def c(self) -> EpGroups:
+        import torch
+        shape = (self.num_experts, self.num_ranks) if self.region_rows else (self.num_experts,)
+        _tensor(self.counts, "counts", torch.int32, shape)
+        if self.offsets is not None:
+            _tensor(self.offsets, "offsets", torch.int32, shape)
+        return EpGroups(_ptr(self.offsets), self.counts.data_ptr(), self.num_experts, self.num_ranks, self.cap_rows,
+                        self.region_rows, self.rows_hint)
+
+
+def _tensor(t, what: str, dtype, shape) -> int:
+    """The pointer of a dense tensor of this type and shape on the current
+    device; anything else is refused (EP_ERR_ARG)."""
+    import torch
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise EpError(EP_ERR_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
+    if not t.is_contiguous():
+        raise EpError(EP_ERR_ARG, f"{what} is not contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise EpError(EP_ERR_ARG, f"{what} is on {t.device}, not on the current GPU")
+    return t.data_ptr()
+
+
+def _shape(t, what: str, dims: int):
+    if t.dim() != dims:
+        raise EpError(EP_ERR_ARG, f"{what}: {t.dim()} dimensions, not {dims}")
+    return tuple(t.shape)
+
+
+def expert_gemm(rows, weights, groups: Groups, row_scales=None, weight_scales=None, out=None):
+    """Grouped product of the received rows with their experts' weights (see
+    ep_expert_gemm in include/ep.h): out [R*cap_rows, N] bf16, rows no expert
+    has not written.
+
+      bf16   rows [R*cap_rows, K], weights [E, N, K] bfloat16
+      FP8    rows [R*cap_rows, K], weights [E, N, K] uint8 (e4m3); float32
+             row_scales [R*cap_rows, K/128] (as dispatch writes them) and
+             weight_scales [E, ceil(N/128), K/128]
+      MXFP4  rows [R*cap_rows, K/2], weights [E, N, K/2] uint8; uint8
+             row_scales [R*cap_rows, K/32], weight_scales [E, N, K/32]
+             (quantize_mxfp4 writes both)
+    """
+    import torch
+    g = groups.c()
+    E, N, width = _shape(weights, "weights", 3)
+    n = groups.num_rows
+    if (row_scales is None) != (weight_scales is None):
+        raise EpError(EP_ERR_ARG, "rows and weights need scales both, or neither")
+    if row_scales is None:
+        form, K, dtype, rs, ws = EP_FORM_BF16, width, torch.bfloat16, None, None
+    elif row_scales.dtype == torch.float32:
+        form, K, dtype = EP_FORM_FP8, width, torch.uint8
+        rs = _tensor(row_scales, "row_scales", torch.float32, (n, K // 128))
+        ws = _tensor(weight_scales, "weight_scales", torch.float32, (groups.num_experts, (N + 127) // 128, K // 128))
+    else:
+        form, K, dtype = EP_FORM_MXFP4, 2 * width, torch.uint8
+        rs = _tensor(row_scales, "row_scales", torch.uint8, (n, K // 32))
+        ws = _tensor(weight_scales, "weight_scales", torch.uint8, (groups.num_experts, N, K // 32))
+    x = _tensor(rows, "rows", dtype, (n, width))
+    w = _tensor(weights, "weights", dtype, (groups.num_experts, N, width))
+    if out is None:
+        out = torch.empty((n, N), dtype=torch.bfloat16, device=rows.device)
+    ep_expert_gemm(g, form, x, rs, w, ws, K, N, _tensor(out, "out", torch.bfloat16, (n, N)), _stream())
+    return out
+
+
+def expert_gemm_dgrad(grad_out, weights, groups: Groups, out=None):
+    """Gradient of the bf16 ``expert_gemm`` in its rows: grad_out [R*cap_rows,
+    N], weights [E, N, K] -> [R*cap_rows, K], all bfloat16."""
+    import torch
+    g = groups.c()
+    E, N, K = _shape(weights, "weights", 3)
+    n = groups.num_rows
+    d = _tensor(grad_out, "grad_out", torch.bfloat16, (n, N))
+    w = _tensor(weights, "weights", torch.bfloat16, (groups.num_experts, N, K))
+    if out is None:
+        out = torch.empty((n, K), dtype=torch.bfloat16, device=weights.device)
+    ep_expert_gemm_dgrad(g, d, w, K, N, _tensor(out, "out", torch.bfloat16, (n, K)), _stream())
+    return out
+
+
+def expert_gemm_wgrad(grad_out, rows, groups: Groups, out=None, dtype=None, accumulate: bool = False):
+    """Gradient of the bf16 ``expert_gemm`` in its weights: grad_out
+    [R*cap_rows, N], rows [R*cap_rows, K] bfloat16 -> [E, N, K] of ``dtype``
+    (float32, the default, or bfloat16; ``out``'s own where it is given).
+    ``accumulate`` adds to a float32 ``out``."""
+    import torch
+    g = groups.c()
+    n, N = _shape(grad_out, "grad_out", 2)
+    _, K = _shape(rows, "rows", 2)
+    if accumulate and out is None:
+        raise EpError(EP_ERR_ARG, "accumulate needs the out to add to")
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise EpError(EP_ERR_ARG, f"out is {out.dtype}, not {dtype}")
+    dtype = out.dtype if out is not None else dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise EpError(EP_ERR_ARG, f"weight gradients are float32 or bfloat16, not {dtype}")
+    d = _tensor(grad_out, "grad_out", torch.bfloat16, (groups.num_rows, N))
+    x = _tensor(rows, "rows", torch.bfloat16, (groups.num_rows, K))
+    shape = (groups.num_experts, N, K)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=rows.device)
+    ep_expert_gemm_wgrad(g, d, x, K, N, _tensor(out, "out", dtype, shape), dtype == torch.float32, accumulate, _stream())
+    return out
+
+
+def swiglu(gate_up, groups: Optional[Groups] = None, kind: str = "bf16", out=None):
+    """silu(gate) * up of rows [num_rows, 2*I] bfloat16 (gate first), between
+    the experts' two products. ``kind`` "bf16" returns [num_rows, I] bfloat16;
+    "fp8" (uint8 e4m3 [num_rows, I], float32 scales [num_rows, I/128]) and
+    "mxfp4" (uint8 [num_rows, I/2], uint8 scales [num_rows, I/32]) return what
+    the next ``expert_gemm`` reads; ``out`` is of the same form. With
+    ``groups`` only the rows experts have are computed and written."""
+    import torch
+    n, I = _shape(gate_up, "gate_up", 2)
+    I //= 2
+    x = _tensor(gate_up, "gate_up", torch.bfloat16, (n, 2 * I))
+    if kind == "bf16":
+        form, spec = EP_FORM_BF16, (((n, I), torch.bfloat16),)
+    elif kind == "fp8":
+        form, spec = EP_FORM_FP8, (((n, I), torch.uint8), ((n, I // 128), torch.float32))
+    elif kind == "mxfp4":
+        form, spec = EP_FORM_MXFP4, (((n, I // 2), torch.uint8), ((n, I // 32), torch.uint8))
+    else:
+        raise EpError(EP_ERR_ARG, f"kind {kind!r} is none of bf16, fp8, mxfp4")
+    outs = (out,) if kind == "bf16" and out is not None else out
+    if outs is None:
+        outs = tuple(torch.empty(s, dtype=t, device=gate_up.device) for s, t in spec)
+    ptrs = [_tensor(o, w, t, s) for o, w, (s, t) in zip(outs, ("out", "scales"), spec)]
+    ep_swiglu(None if groups is None else groups.c(), x, n, I, form, ptrs[0], ptrs[1] if len(ptrs) > 1 else None,
+              _stream())
+    return outs[0] if kind == "bf16" else tuple(outs)
+
+
+def swiglu_backward(grad_out, gate_up, groups: Optional[Groups] = None, out=None):
+    """Gradient of ``swiglu`` in gate_up [num_rows, 2*I]: grad_out [num_rows,
+    I] -> [num_rows, 2*I], all bfloat16. ``out`` may be ``gate_up``."""
+    import torch
+    n, I = _shape(grad_out, "grad_out", 2)
+    d = _tensor(grad_out, "grad_out", torch.bfloat16, (n, I))
+    x = _tensor(gate_up, "gate_up", torch.bfloat16, (n, 2 * I))
+    if out is None:
+        out = torch.empty((n, 2 * I), dtype=torch.bfloat16, device=gate_up.device)
+    ep_swiglu_backward(None if groups is None else groups.c(), d, x, n, I,
+                       _tensor(out, "out", torch.bfloat16, (n, 2 * I)), _stream())
+    return out
+
+
+def quantize_mxfp4(x, groups: Optional[Groups] = None, out=None):
+    """MXFP4 form of the bfloat16 rows of x [..., cols] (weights [E, N, K] as
+    well as rows): (uint8 [..., cols/2], uint8 scales [..., cols/32]). With
+    ``groups`` (x [R*cap_rows, cols]) only the rows experts have."""
+    import torch
+    cols = x.shape[-1] if x.dim() else 0
+    n = x.numel() // cols if cols else 0
+    p = _tensor(x, "x", torch.bfloat16, x.shape)
+    shapes = tuple(x.shape[:-1]) + (cols // 2,), tuple(x.shape[:-1]) + (cols // 32,)
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.uint8, device=x.device) for s in shapes)
+    q, scales = out
+    ep_quantize_mxfp4(None if groups is None else groups.c(), p, n, cols, _tensor(q, "q", torch.uint8, shapes[0]),
+                      _tensor(scales, "scales", torch.uint8, shapes[1]), _stream())
+    return q, scales
+
+
+def dequantize_mxfp4(q, scales, groups: Optional[Groups] = None, out=None):
+    """The bfloat16 values [..., cols] that quantize_mxfp4's (q, scales) stand for."""
+    import torch
+    cols = 2 * q.shape[-1] if q.dim() else 0
+    n = 2 * q.numel() // cols if cols else 0
+    shape = tuple(q.shape[:-1]) + (cols,)
+    p = _tensor(q, "q", torch.uint8, q.shape)
+    s = _tensor(scales, "scales", torch.uint8, tuple(q.shape[:-1]) + (cols // 32,))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    ep_dequantize_mxfp4(None if groups is None else groups.c(), p, s, n, cols,
+                        _tensor(out, "out", torch.bfloat16, shape), _stream())
+    return out
 
 
 class CuStream:

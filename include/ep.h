@@ -413,6 +413,117 @@ int ep_pattern_push(const uint16_t *x, const int32_t *pos, void *rows, int num_t
 int ep_pattern_gather(const uint16_t *rows, const int32_t *pos, uint16_t *out, int num_tokens, int num_topk,
                       int hidden, int64_t num_rows, int capped, ep_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The experts' side: what a rank computes on its received rows between the
+ * dispatch and the combine. These calls take no context and no workspace, and
+ * allocate nothing: any number may run at once, on any streams, and each may
+ * be captured in a HIP graph. They run on the current device, whose memory
+ * all their pointers must be.
+ *
+ * ep_groups says which receive rows are whose (a host struct; the counts and
+ * offsets stay on the device and are read when the call runs):
+ *  - region_rows = 0, the packed layout of ep_dispatch: expert e lives on rank
+ *    d = e / (num_experts / num_ranks), its rows are d*cap_rows + offsets[e] +
+ *    [0, counts[e]): offsets = layout.expert_off, counts = layout.recv_cnt.
+ *    Rows past the rank's cap_rows (which the dispatch dropped) are left out.
+ *  - region_rows = T/R > 0, the layout of ep_dispatch_low_latency: expert e's
+ *    rows are e*num_ranks*region_rows + s*region_rows + [0, counts[e][s]) for
+ *    each source s: counts = recv_count, offsets NULL, cap_rows =
+ *    num_experts * region_rows.
+ * Negative counts or offsets and counts past a region are cut to the region,
+ * so no call leaves the row arrays whatever the device arrays hold. Experts'
+ * rows must not overlap (the layouts' never do): rows two experts claim get
+ * either's result. Rows no expert has are neither read into a result nor
+ * written.
+ * rows_hint: about how many rows the groups hold together (T*k for a
+ * dispatch), from which the tile sizes are chosen; 0 = unknown (then
+ * num_ranks*cap_rows). Any value gives right results. The choice can change
+ * the order of a sum's fp32 additions, nothing else does: the same call on
+ * the same data gives the same bits.
+ * Limits: 1 <= num_experts <= 1024, 1 <= num_ranks <= 64, num_experts %
+ * num_ranks == 0, num_ranks*cap_rows < 2^31; 8 <= channels <= 65536,
+ * channels % 8 == 0 (% 128 along the reduction of FP8 and MXFP4 products). */
+typedef struct {
+    const int32_t *offsets; /* [E], or NULL with region_rows > 0 */
+    const int32_t *counts;  /* [E], or [E][R] with region_rows > 0 */
+    int32_t num_experts;    /* E */
+    int32_t num_ranks;      /* R */
+    int64_t cap_rows;       /* receive rows per rank */
+    int64_t region_rows;    /* 0: packed; else rows per (expert, source) region */
+    int64_t rows_hint;
+} ep_groups;
+
+/* number formats of a product's operands */
+#define EP_FORM_BF16 0
+#define EP_FORM_FP8 1   /* e4m3fn bytes, fp32 scales: rows one per 128 channels, weights one per 128 x 128 block */
+#define EP_FORM_MXFP4 2 /* e2m1 values, two per byte (the even channel in the low half), e8m0 scales per 32 channels */
+
+/* Grouped product: for every row p of expert e and n < N,
+ *   out[p][n] = bf16_rne(sum_k W[e][n][k] * row[p][k]),
+ * products exact, sums in fp32.
+ *   BF16: rows [R*cap_rows][K], weights [E][N][K] bf16; scales NULL.
+ *   FP8: rows [R*cap_rows][K] e4m3 with row_scales [R*cap_rows][K/128] fp32, as
+ *     ep_dispatch writes them; weights [E][N][K] e4m3 with weight_scales
+ *     [E][ceil(N/128)][K/128] fp32. Each block of 128 channels is summed
+ *     unscaled, then added times (row scale * weight scale). (The matrix
+ *     unit's sum of 128 FP8 products is aligned to the largest of them and
+ *     keeps fewer bits below it than fp32 does.)
+ *   MXFP4: rows [R*cap_rows][K/2] and weights [E][N][K/2] bytes with scales
+ *     [..][K/32] bytes, a scale byte b standing for 2^(b-127), 255 for NaN
+ *     (ep_quantize_mxfp4 writes both).
+ * out: [R*cap_rows][N]. Rows, weights and out 16-byte aligned, scales 4-byte. */
+int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const void *row_scales, const void *weights,
+                   const void *weight_scales, int K, int N, uint16_t *out, ep_stream_t stream);
+
+/* Gradient of the BF16 product in its rows: for every row p of expert e,
+ * grad_rows[p][k] = bf16_rne(sum_n grad_out[p][n] * W[e][n][k]).
+ * grad_out: [R*cap_rows][N]; weights [E][N][K] as in the forward call;
+ * grad_rows: [R*cap_rows][K]. All 16-byte aligned. */
+int ep_expert_gemm_dgrad(const ep_groups *groups, const uint16_t *grad_out, const uint16_t *weights, int K, int N,
+                         uint16_t *grad_rows, ep_stream_t stream);
+
+/* Gradient of the BF16 product in its weights: for every expert e (zero rows:
+ * zeros), grad_weights[e][n][k] = sum over e's rows p of grad_out[p][n] *
+ * row[p][k], summed in fp32. grad_weights: [E][N][K], fp32 (out_f32 = 1) or
+ * bf16; accumulate = 1 (fp32 only) adds to what it holds. All 16-byte aligned. */
+int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, const uint16_t *rows, int K, int N,
+                         void *grad_weights, int out_f32, int accumulate, ep_stream_t stream);
+
+/* SwiGLU between the experts' two products: h[p][i] = silu(gate) * up with
+ * gate = gate_up[p][i], up = gate_up[p][I + i], silu(g) = g / (1 + exp(-g)),
+ * in fp32, for every row p that an expert has (groups NULL: all num_rows rows).
+ * gate_up: [num_rows][2*I] bf16; num_rows = R*cap_rows where groups are given.
+ *   EP_FORM_BF16: out [num_rows][I] bf16; scales NULL.
+ *   EP_FORM_FP8: out bytes [num_rows][I], scales fp32 [num_rows][I/128], by the
+ *     dispatch's rule (I % 128 == 0); a group that holds a NaN or an infinity
+ *     gets a NaN scale and NaN codes.
+ *   EP_FORM_MXFP4: out bytes [num_rows][I/2], scales bytes [num_rows][I/32], by
+ *     ep_quantize_mxfp4's rule (I % 32 == 0).
+ * h is not rounded to bf16 before it is quantized. 16-byte alignment. */
+int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows, int I, int form, void *out,
+              void *scales, ep_stream_t stream);
+
+/* Its gradient, with s = 1 / (1 + exp(-gate)): grad_gate_up[p][i] =
+ * grad_out[p][i] * up * s * (1 + gate * (1 - s)) and grad_gate_up[p][I + i] =
+ * grad_out[p][i] * gate * s, in fp32, rounded to bf16. grad_gate_up may be
+ * gate_up itself. */
+int ep_swiglu_backward(const ep_groups *groups, const uint16_t *grad_out, const uint16_t *gate_up, int64_t num_rows,
+                       int I, uint16_t *grad_gate_up, ep_stream_t stream);
+
+/* MXFP4 quantization of bf16 rows x [num_rows][cols] (cols % 32 == 0): per 32
+ * channels, e = floor(log2(max |x|)) - 2 (at least -127; zeros: -127), scale
+ * byte e + 127, and each value x / 2^e rounded to the nearest of 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 with its sign (ties to the even code, magnitudes past 6 to
+ * 6). A group that holds a NaN or an infinity gets the scale byte 255 (NaN)
+ * and zero codes. q: [num_rows][cols/2] bytes, scales: [num_rows][cols/32]
+ * bytes. groups NULL: every row; else the rows experts have (num_rows =
+ * R*cap_rows). ep_dequantize_mxfp4 is the way back, exact in bf16. x and q
+ * 16-byte aligned. */
+int ep_quantize_mxfp4(const ep_groups *groups, const uint16_t *x, int64_t num_rows, int cols, uint8_t *q,
+                      uint8_t *scales, ep_stream_t stream);
+int ep_dequantize_mxfp4(const ep_groups *groups, const uint8_t *q, const uint8_t *scales, int64_t num_rows, int cols,
+                        uint16_t *x, ep_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
