@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ep.h"
 #include "ep_groups.h"
 
@@ -53,16 +55,25 @@ struct ProductArgs {
 // copies to LDS and waits
 // ---------------------------------------------------------------------------
 
-// Copy 16 (4) bytes per lane from `src` to LDS at `lds` + 16 (4) * lane; `lds`
-// is the same in every lane. Written as asm because the compiler, which
-// cannot tell the ring's buffers apart, otherwise waits for all copies in
-// flight before every LDS read; the instruction has no result register, and
-// the waits are wait_copies() below. M0 holds the LDS address and needs one
-// wait state before its use.
-__device__ __forceinline__ void copy16(const void *src, uint32_t lds) {
+// Copy 16 (4) bytes per lane from base + off to LDS at `lds` + 16 (4) * lane;
+// base and lds are the same in every lane. Written as asm because the
+// compiler, which cannot tell the ring's buffers apart, otherwise waits for
+// all copies in flight before every LDS read; the instruction has no result
+// register, and the waits are wait_copies() below. M0 holds the LDS address
+// and needs one wait state before its use.
+__device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(const uint8_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory");
+}
+// the same with an address per lane
+__device__ __forceinline__ void copy16(const uint8_t *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
 }
-__device__ __forceinline__ void copy4(const void *src, uint32_t lds) {
+__device__ __forceinline__ void copy4(const uint8_t *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory");
 }
 
@@ -73,12 +84,23 @@ __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Keep the compiler from moving instructions across.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-__device__ __forceinline__ i32x4 read16(uint32_t a) {
-    return *(const __attribute__((address_space(3))) i32x4 *)(uintptr_t)a;
+// a pointer that is the same in every lane, as the copies' base has to be
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t *)((uint64_t)hi << 32 | lo);
+}
+
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t a) {
+    return *(const __attribute__((address_space(3))) T *)(uintptr_t)a;
 }
 
 __device__ __forceinline__ uint16_t bf16_of(float f) {
@@ -91,15 +113,23 @@ __device__ __forceinline__ uint16_t bf16_of(float f) {
 // operand tiles in LDS
 // ---------------------------------------------------------------------------
 
-// Reduction-contiguous operand: ROWS rows of 128 bytes. Chunk c (16 bytes) of
-// row r is at slot c ^ (r & 7), so that eight neighbouring rows' same chunk
-// fall on different banks. A wave copies 8 rows per instruction, lane l taking
-// slot l & 7 of row l >> 3.
+// Reduction-contiguous operand: rows of 128 bytes. Chunk c (16 bytes) of row r
+// is at slot c ^ (r & 7), so that eight neighbouring rows' same chunk fall on
+// different banks. A wave copies 8 rows per instruction, lane l taking slot
+// l & 7 of row l >> 3.
 //
 // Reduction-strided operand (TR): 64 reduction rows of COLS bf16. The 32-byte
 // unit u of row r is at u ^ f(r), f = (r & 3) | (r >> 3 & 1) << 2: the sixteen
 // rows one transposing read touches spread over all banks.
 __device__ __forceinline__ int tr_swizzle(int r) { return (r & 3) | ((r >> 1) & 4); }
+
+// the column (of COLS) and row that lane `lane` of copy `ins` of a TR tile takes
+template <int COLS>
+__device__ __forceinline__ void tr_place(int ins, int lane, int &row, int &col) {
+    const int at = ins * 64 + lane, pc = at % (COLS / 8);
+    row = at / (COLS / 8);
+    col = ((((pc >> 1) ^ tr_swizzle(row)) << 1) | (pc & 1)) * 8;
+}
 
 // bf16 fragment (8 reduction values of one column) of column tile `ct` and
 // 32-value step s from a TR tile of COLS columns
@@ -118,297 +148,499 @@ __device__ __forceinline__ i32x4 read_tr(uint32_t tile, int ct, int s) {
     return __builtin_bit_cast(i32x4, both);
 }
 
-__device__ __forceinline__ f32x4 mfma_bf16(i32x4 a, i32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-
 __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
     return i32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
+
+// the host pass parses device code, and knows another register of this name
+#if defined(__HIP_DEVICE_COMPILE__)
+#define EP_ACC "+a"
+#else
+#define EP_ACC "+m"
+#endif
+
+// c += a b. ACC: the accumulators of a wave that has a SIMD to itself live in
+// its accumulation registers and everything else in the others, which the
+// compiler does not manage by itself for so many (it moves them about within
+// the loop). Written as asm, the instructions are outside the compiler's
+// hazard tracking: their operands come from LDS reads alone (which it does
+// track), and settle() ends every step that can be a tile's last.
+template <bool ACC>
+__device__ __forceinline__ void mfma_bf16(i32x4 a, i32x4 b, f32x4 &c) {
+    if constexpr (ACC)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : EP_ACC(c) : "v"(a), "v"(b));
+    else
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                    0, 0);
+}
+
+// as: the scale byte of the lane's 32 values of a, in the word's low byte
+template <bool ACC>
+__device__ __forceinline__ void mfma_mx4(i32x4 a, i32x4 b, f32x4 &c, int as, int bs) {
+    if constexpr (ACC) {
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : EP_ACC(c)
+                     : "v"(a), "v"(b), "v"(as), "v"(bs));
+    } else {
+        const i32x4 z = {0, 0, 0, 0};
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(a, z), join(b, z), c, 4, 4, 0, as, 0, bs);
+    }
+}
+
+// the last matrix instructions' results have reached the registers (at most 16 passes of 4 cycles)
+__device__ __forceinline__ void settle() {
+    pin();
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    pin();
+}
+
+// ---------------------------------------------------------------------------
+// the reduction
+// ---------------------------------------------------------------------------
+
+// The ring's first steps: whole ones, then those with chunks past the end.
+template <class P>
+__device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, int whole) {
+#pragma unroll
+    for (int i = 0; i < P::kStages; ++i) {
+        if (i < whole) {
+#pragma unroll
+            for (int c = 0; c < P::kPer; ++c) p.template copy<true>(i, ring + i * P::kStage, c);
+        } else if (i < steps) {
+#pragma unroll
+            for (int c = 0; c < P::kPer; ++c) p.template copy<false>(i, ring + i * P::kStage, c);
+        }
+    }
+}
+
+enum Copies { kNone, kWhole, kPartial };
+
+// One tile's reduction for a wave: acc[i][j] += the products of the rows'
+// side fragment i < ACT and the weights' side fragment j < NT over all steps,
+// the first `whole` of which need no check for the end of the rows. A step is
+// two halves of 64 bytes per row. While one half's matrix instructions run,
+// the next half's fragments are read into registers (and the MXFP4 form's
+// scales with them), and the copies of the step kStages ahead are issued; the workgroup meets once a step, in its
+// middle, when the step's buffer has been read out and the next one's must
+// have landed. The order of the source is kept (pin): a few matrix
+// instructions, then a read or a copy, and so on, so that the matrix unit
+// always has work queued. (The last step reads a next one that is none;
+// nothing uses it.)
+template <class P>
+__device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
+    constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
+    fill_ring(p, ring, steps, whole);
+    if (S <= steps)
+        wait_copies<(S - 1) * P::kPer>();
+    else
+        wait_copies<0>();
+    typename P::Frags h0, h1;
+#pragma unroll
+    for (int f = 0; f < P::kReads; ++f) p.read(h0, ring, f, 0);
+    int slot = 0, step = 0;
+    auto body = [&](auto copies) __attribute__((always_inline)) {
+        constexpr int COPIES = decltype(copies)::value;
+        constexpr int M = ACT * NT, I1 = P::kReads, I2 = P::kReads + (COPIES != kNone ? P::kPer : 0);
+        const uint32_t st = ring + slot * P::kStage;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        const uint32_t nx = ring + slot * P::kStage;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int f = m * I1 / M; f < (m + 1) * I1 / M; ++f) p.read(h1, st, f, 1);
+            p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
+            if (m % 2) pin();
+        }
+        wait_copies<(COPIES == kNone ? 0 : (S - 2) * P::kPer)>();
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int f = m * I2 / M; f < (m + 1) * I2 / M; ++f) {
+                // reads and copies in turn
+                const int c = f * P::kPer / I2;
+                if (COPIES != kNone && (f + 1) * P::kPer / I2 > c)
+                    p.template copy<COPIES == kWhole>(step + S, st, c);
+                else
+                    p.read(h0, nx, COPIES != kNone ? f - c : f, 0);
+            }
+            p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
+            if (m % 2) pin();
+        }
+        if (P::kAcc && COPIES == kNone) settle();
+        ++step;
+    };
+    while (step + S < whole) body(std::integral_constant<int, kWhole>());
+    while (step + S < steps) body(std::integral_constant<int, kPartial>());
+    while (step < steps) body(std::integral_constant<int, kNone>());
+}
+
+// The FP8 form's reduction: a step is one block of 128 channels, its products
+// of a row tile summed by one matrix instruction from zero and added times
+// the row's and the weights' scale. Fragments are read two row tiles ahead
+// and added one row tile behind. (K is a multiple of 128: all steps are whole.)
+template <class P>
+__device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps, constant_f32 w_scales,
+                                           f32x4 (&acc)[P::ACT][P::NT]) {
+    constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
+    fill_ring(p, ring, steps, steps);
+    int slot = 0, step = 0;
+    float ws = w_scales[0];
+    auto body = [&](auto copies) __attribute__((always_inline)) {
+        constexpr int COPIES = decltype(copies)::value;
+        wait_copies<(COPIES == kNone ? 0 : (S - 1) * P::kPer)>();
+        const uint32_t st = ring + slot * P::kStage;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        i32x8 w[NT], x[3];
+        float s[4];  // one more than the fragments: used a row tile later
+        f32x4 part[2][NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w[j] = join(p.w(st, j, 0), p.w(st, j, 1));
+#pragma unroll
+        for (int i = 0; i < (ACT < 2 ? ACT : 2); ++i) {
+            x[i] = join(p.x(st, i, 0), p.x(st, i, 1));
+            s[i] = p.x_scale(st, i);
+        }
+        pin();
+#pragma unroll
+        for (int i = 0; i < ACT; ++i) {
+            if (i + 2 < ACT) {
+                x[(i + 2) % 3] = join(p.x(st, i + 2, 0), p.x(st, i + 2, 1));
+                s[(i + 2) % 4] = p.x_scale(st, i + 2);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                part[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    w[j], x[i % 3], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+            if (i > 0) {
+                const float f = s[(i - 1) % 4] * ws;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i - 1][j][q] = fmaf(part[(i - 1) & 1][j][q], f, acc[i - 1][j][q]);
+            }
+            pin();
+        }
+        const float f = s[(ACT - 1) % 4] * ws;
+        ws = w_scales[step + 1 < steps ? step + 1 : step];
+        if (COPIES != kNone) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffer has been read out
+#pragma unroll
+            for (int c = 0; c < P::kPer; ++c) p.template copy<true>(step + S, st, c);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[ACT - 1][j][q] = fmaf(part[(ACT - 1) & 1][j][q], f, acc[ACT - 1][j][q]);
+        ++step;
+    };
+    while (step + S < steps) body(std::integral_constant<int, kWhole>());
+    while (step < steps) body(std::integral_constant<int, kNone>());
+}
+
+// One half's fragments: weights' side, rows' side, MXFP4 scales of both.
+template <int ACT, int NT, bool SCALES>
+struct HalfFrags {
+    i32x4 w[NT], x[ACT];
+    int ws[SCALES ? NT : 1], xs[SCALES ? ACT : 1];
+};
 
 // ---------------------------------------------------------------------------
 // product and dgrad
 // ---------------------------------------------------------------------------
 
-template <int FORM, bool WTR, int BM, int BN, int WM, int WN, int STAGES>
+// A tile: up to MOST = 16 * WM * MT rows of one expert by BN channels, by WM x
+// WN waves. Row tiles of 16 are dealt to the WM waves in turn, so that a tile
+// with few rows costs each of them as little, in steps of half, a quarter, an
+// eighth (ACT row tiles per wave), of rows copied as well as multiplied.
+template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
 struct Product {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-    static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 tiles per wave
-    static constexpr int kXBytes = BM * kStepBytes, kWBytes = BN * kStepBytes;
-    // scales of one step in LDS: FP8 one float per row; MX4 eight bytes per row of both sides
-    static constexpr int kXScale = FORM == kFp8 ? (BM < 64 ? 64 : BM) * 4 : FORM == kMx4 ? (BM < 32 ? 32 : BM) * 8 : 0;
-    static constexpr int kWScale = FORM == kMx4 ? BN * 8 : 0;
-    static constexpr int kStage = kXBytes + kWBytes + kXScale + kWScale;
-    // copies per wave and step: a multiple for all waves, so that one count of copies in flight holds for each
-    static constexpr int kXIns = kXBytes / 1024, kWIns = kWBytes / 1024;
-    static constexpr int kXPer = (kXIns + kWaves - 1) / kWaves, kWPer = (kWIns + kWaves - 1) / kWaves;
-    static constexpr int kXsIns = kXScale / 256, kWsIns = kWScale / 256;
-    static constexpr int kXsPer = (kXsIns + kWaves - 1) / kWaves, kWsPer = (kWsIns + kWaves - 1) / kWaves;
-    static constexpr int kPer = kXPer + kWPer + kXsPer + kWsPer;
-    static_assert(MT >= 1 && NT >= 1 && STAGES >= 2, "tile");
+    static constexpr int MOST = 16 * WM * MT, NTILES = BN / 16 / WN;
+    static constexpr bool kAccumulate = MT * NTILES >= 64;  // 256 accumulators a lane: all registers of a SIMD
+    static constexpr int kRing = BN >= 256 ? 144 * 1024 : 72 * 1024;
     static_assert(!WTR || FORM == kBf16, "only bf16 has a transposing read");
 
     struct Shared {
-        uint8_t ring[STAGES][kStage];
+        uint8_t ring[kRing];
         int ends[ep::kGroupsMaxExperts];
-        int row[BM];
+        int row[MOST];
+        int tiles[3];
     };
 
-    // this wave's sources: kXPer + kWPer chunks per lane, advanced by the step
-    struct Sources {
-        const uint8_t *x[kXPer], *w[kWPer];
-        const uint8_t *xs[kXsPer > 0 ? kXsPer : 1], *ws[kWsPer > 0 ? kWsPer : 1];
-    };
+    // what a wave needs to copy and read a tile's steps, for ACT row tiles per wave
+    template <int ACT_>
+    struct Tile {
+        static constexpr int ACT = ACT_, NT = NTILES, ROWS = 16 * WM * ACT;
+        static constexpr int kXBytes = ROWS * kStepBytes, kWBytes = BN * kStepBytes;
+        // scales of one step: FP8 one float per row; MX4 eight bytes per row of both sides
+        static constexpr int kXScale = FORM == kFp8 ? (ROWS < 64 ? 64 : ROWS) * 4 : FORM == kMx4 ? ROWS * 8 : 0;
+        static constexpr int kWScale = FORM == kMx4 ? BN * 8 : 0;
+        static constexpr int kStage = kXBytes + kWBytes + kXScale + kWScale;
+        static constexpr int kStages = kRing / kStage < 4 ? kRing / kStage : 4;
+        // copies per step; every wave issues as many (some repeat another's), so that one count of copies in flight
+        // holds for each
+        static constexpr int kXIns = kXBytes / 1024, kWIns = kWBytes / 1024;
+        static constexpr int kXPer = (kXIns + kWaves - 1) / kWaves, kWPer = (kWIns + kWaves - 1) / kWaves;
+        static constexpr int kXsIns = kXScale / 256, kWsIns = kWScale / 256;
+        static constexpr int kXsPer = (kXsIns + kWaves - 1) / kWaves, kWsPer = (kWsIns + kWaves - 1) / kWaves;
+        static constexpr int kPer = kXPer + kWPer + kXsPer + kWsPer;
+        static_assert(kStages >= 2 && kPer * (kStages - 1) < 64, "ring");
+        using Frags = HalfFrags<ACT, NT, FORM == kMx4>;
+        static constexpr int kReads = (FORM == kMx4 ? 2 : 1) * (ACT + NT);
+        static constexpr bool kAcc = kAccumulate;
 
-    static __device__ __forceinline__ int x_ins(int wave, int i) { return (wave + i * kWaves) % kXIns; }
-    static __device__ __forceinline__ int w_ins(int wave, int i) { return (wave + i * kWaves) % kWIns; }
+        // sources: one base per operand, offsets within the tile per lane
+        const uint8_t *xb, *wb, *xsb, *wsb;
+        uint32_t xo[kXPer], wo[kWPer], xso[kXsPer > 0 ? kXsPer : 1], wso[kWsPer > 0 ? kWsPer : 1];
+        int64_t wstep;   // bytes of the weights' base per step
+        int row_bytes;   // of a reduction-contiguous row
+        int wave, lane, K;
+        // LDS offsets of this lane's reads
+        uint32_t xr, wr, half[2];
 
-    static __device__ __forceinline__ void copy_step(const ProductArgs &a, const Sources &src, uint32_t stage, int step,
-                                                     int wave, int lane, int n0) {
-        const int64_t rowbytes = FORM == kBf16 ? (int64_t)a.K * 2 : FORM == kFp8 ? a.K : a.K / 2;
-        const int64_t at = (int64_t)step * kStepBytes;
-        const bool whole = at + kStepBytes <= rowbytes;
-        const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // of a reduction-contiguous tile: row & 7 == lane >> 3
-        const bool in = whole || at + chunk < rowbytes;
+        __device__ __forceinline__ Tile(const ProductArgs &a, const Shared &sh, int wave_, int lane_, int e, int n0)
+            : wave(wave_), lane(lane_), K(a.K) {
+            const int64_t row0 = __builtin_amdgcn_readfirstlane(sh.row[0]);
+            row_bytes = FORM == kBf16 ? a.K * 2 : FORM == kFp8 ? a.K : a.K / 2;
+            xb = uniform(a.x + row0 * row_bytes);
+            const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
-        for (int i = 0; i < kXPer; ++i)
-            copy16(in ? (const void *)(src.x[i] + at) : (const void *)&k_zero_chunk, stage + x_ins(wave, i) * 1024);
-#pragma unroll
-        for (int i = 0; i < kWPer; ++i) {
-            const int ins = w_ins(wave, i);
-            const uint8_t *p;
-            if (WTR) {  // 64 reduction rows of BN columns: the step's rows past the end are zeros
-                const int r = (ins * 64 + lane) / (BN / 8);
-                const bool ok = step * 64 + r < a.K;
-                p = ok ? src.w[i] + (int64_t)step * 64 * a.N * 2 : (const uint8_t *)&k_zero_chunk;
-            } else {
-                p = in ? src.w[i] + at : (const uint8_t *)&k_zero_chunk;
-            }
-            copy16(p, stage + kXBytes + ins * 1024);
-        }
-        if constexpr (FORM == kFp8) {
-#pragma unroll
-            for (int i = 0; i < kXsPer; ++i)
-                copy4(src.xs[i] + step * 4, stage + kXBytes + kWBytes + ((wave + i * kWaves) % kXsIns) * 256);
-        }
-        if constexpr (FORM == kMx4) {
-            // two words of four scales per row and step; the last step may have one
-            const bool ok = step * 8 + (lane & 1) * 4 < a.K / 32;
-#pragma unroll
-            for (int i = 0; i < kXsPer; ++i)
-                copy4(ok ? src.xs[i] + step * 8 : (const uint8_t *)&k_zero_chunk,
-                      stage + kXBytes + kWBytes + ((wave + i * kWaves) % kXsIns) * 256);
-#pragma unroll
-            for (int i = 0; i < kWsPer; ++i)
-                copy4(ok ? src.ws[i] + step * 8 : (const uint8_t *)&k_zero_chunk,
-                      stage + kXBytes + kWBytes + kXScale + ((wave + i * kWaves) % kWsIns) * 256);
-        }
-    }
-
-    // one step's products of the wave's first ACT row tiles
-    template <int ACT>
-    static __device__ __forceinline__ void multiply(uint32_t stage, float w_scale, int wm, int wn, int lane,
-                                                    f32x4 (&acc)[MT][NT]) {
-        const int g = lane >> 4, r = lane & 15;
-        const uint32_t xt = stage + r * kStepBytes, wt = stage + kXBytes + r * kStepBytes;
-        if constexpr (FORM == kFp8) {
-            const uint32_t lo = (g ^ (r & 7)) * 16, hi = ((g + 4) ^ (r & 7)) * 16;
-            i32x8 wf[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint32_t t = wt + (wn * NT + j) * 16 * kStepBytes;
-                wf[j] = join(read16(t + lo), read16(t + hi));
+            for (int i = 0; i < kXPer; ++i)
+                xo[i] = (uint32_t)(sh.row[(wave + i * kWaves) % kXIns * 8 + (lane >> 3)] - (int)row0) * row_bytes + chunk;
+            if (WTR) {  // W[e] is [K reduction rows][N columns]; columns past the end repeat the last chunk
+                wb = uniform(a.w + ((int64_t)e * a.K * a.N + n0) * 2);
+                wstep = (int64_t)64 * a.N * 2;
+            } else {  // rows past the end repeat the last one
+                wb = uniform(a.w + ((int64_t)e * a.N + n0) * row_bytes);
+                wstep = kStepBytes;
             }
 #pragma unroll
-            for (int i = 0; i < ACT; ++i) {
-                const uint32_t t = xt + (wm + i * WM) * 16 * kStepBytes;
-                const i32x8 xf = join(read16(t + lo), read16(t + hi));
-                const float s = w_scale * *(const __attribute__((address_space(3))) float *)(uintptr_t)(
-                                              stage + kXBytes + kWBytes + ((wm + i * WM) * 16 + r) * 4);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[j], xf, f32x4{0, 0, 0, 0}, 0, 0,
-                                                                                     0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(p[q], s, acc[i][j][q]);
+            for (int i = 0; i < kWPer; ++i) {
+                const int ins = (wave + i * kWaves) % kWIns;
+                if (WTR) {
+                    int r, c;
+                    tr_place<BN>(ins, lane, r, c);
+                    wo[i] = ((uint32_t)r * a.N + min(c, a.N - 8 - n0)) * 2;
+                } else {
+                    wo[i] = (uint32_t)min(ins * 8 + (lane >> 3), a.N - 1 - n0) * row_bytes + chunk;
                 }
             }
-        } else {
-            int wsc[NT], xsc[ACT];
+            xsb = wsb = nullptr;
+            if constexpr (FORM == kFp8) {
+                xsb = uniform(a.x_scales + row0 * (a.K / 128) * 4);
+#pragma unroll
+                for (int i = 0; i < kXsPer; ++i)
+                    xso[i] = (uint32_t)(sh.row[min((wave + i * kWaves) % kXsIns * 64 + lane, ROWS - 1)] - (int)row0) *
+                             (a.K / 128) * 4;
+            }
             if constexpr (FORM == kMx4) {
-                const uint32_t st = stage + kXBytes + kWBytes;
+                xsb = uniform(a.x_scales + row0 * (a.K / 32));
+                wsb = uniform(a.w_scales + ((int64_t)e * a.N + n0) * (a.K / 32));
 #pragma unroll
-                for (int i = 0; i < ACT; ++i)
-                    xsc[i] = *(const __attribute__((address_space(3))) uint16_t *)(uintptr_t)(
-                        st + ((wm + i * WM) * 16 + r) * 8 + g * 2);
+                for (int i = 0; i < kXsPer; ++i)
+                    xso[i] = (uint32_t)(sh.row[(wave + i * kWaves) % kXsIns * 32 + (lane >> 1)] - (int)row0) * (a.K / 32) +
+                             (lane & 1) * 4;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    wsc[j] = *(const __attribute__((address_space(3))) uint16_t *)(uintptr_t)(
-                        st + kXScale + ((wn * NT + j) * 16 + r) * 8 + g * 2);
+                for (int i = 0; i < kWsPer; ++i)
+                    wso[i] = (uint32_t)min((wave + i * kWaves) % kWsIns * 32 + (lane >> 1), a.N - 1 - n0) * (a.K / 32) +
+                             (lane & 1) * 4;
             }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                // MX4: a lane's two chunks are neighbours, as are their scales in one 16-bit word
-                const uint32_t c = ((FORM == kMx4 ? 2 * g + s : 4 * s + g) ^ (r & 7)) * 16;
-                i32x4 wf[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    wf[j] = WTR ? read_tr<BN>(stage + kXBytes, wn * NT + j, s)
-                                : read16(wt + (wn * NT + j) * 16 * kStepBytes + c);
-#pragma unroll
-                for (int i = 0; i < ACT; ++i) {
-                    const i32x4 xf = read16(xt + (wm + i * WM) * 16 * kStepBytes + c);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if constexpr (FORM == kBf16) {
-                            acc[i][j] = mfma_bf16(wf[j], xf, acc[i][j]);
-                        } else {
-                            const i32x4 z = {0, 0, 0, 0};
-                            if (s == 0)
-                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                    join(wf[j], z), join(xf, z), acc[i][j], 4, 4, 0, wsc[j], 0, xsc[i]);
-                            else
-                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                    join(wf[j], z), join(xf, z), acc[i][j], 4, 4, 1, wsc[j], 1, xsc[i]);
-                        }
-                    }
+            const int g = lane >> 4, r = lane & 15, wm = wave / WN, wn = wave % WN;
+            xr = wm * 16 * kStepBytes + r * kStepBytes;
+            wr = kXBytes + (wn * NT * 16 + r) * kStepBytes;
+            // chunks of the two halves: MX4's are neighbours, as are their scales
+            half[0] = ((FORM == kMx4 ? 2 * g : g) ^ (r & 7)) * 16;
+            half[1] = ((FORM == kMx4 ? 2 * g + 1 : g + 4) ^ (r & 7)) * 16;
+        }
+
+        // the wave's c-th copy of a step into the buffer at `stage`; WHOLE: no chunk of the step lies past the end (those
+        // come from zeros)
+        template <bool WHOLE>
+        __device__ __forceinline__ void copy(int step, uint32_t stage, int c) const {
+            const int64_t at = (int64_t)step * kStepBytes;
+            const uint8_t *zero = (const uint8_t *)&k_zero_chunk;
+            const bool in = WHOLE || (int)at + (((lane & 7) ^ (lane >> 3)) * 16) < row_bytes;
+            if (c < kXPer) {
+                const uint32_t to = stage + (wave + c * kWaves) % kXIns * 1024;
+                if (WHOLE)
+                    copy16(xb + at, xo[c], to);
+                else
+                    copy16(in ? xb + at + xo[c] : zero, to);
+            } else if (c < kXPer + kWPer) {
+                const int i = c - kXPer, ins = (wave + i * kWaves) % kWIns;
+                const uint32_t to = stage + kXBytes + ins * 1024;
+                if (WHOLE) {
+                    copy16(wb + step * wstep, wo[i], to);
+                } else {
+                    const bool ok = WTR ? step * 64 + (ins * 64 + lane) / (BN / 8) < K : in;
+                    copy16(ok ? wb + step * wstep + wo[i] : zero, to);
                 }
+            } else if (c < kXPer + kWPer + kXsPer) {
+                const int i = c - kXPer - kWPer;
+                const uint32_t to = stage + kXBytes + kWBytes + (wave + i * kWaves) % (kXsIns > 0 ? kXsIns : 1) * 256;
+                if constexpr (FORM == kFp8) copy4(xsb + step * 4, xso[i], to);
+                if constexpr (FORM == kMx4) {
+                    if (WHOLE)
+                        copy4(xsb + step * 8, xso[i], to);
+                    else  // half a step: one word of four scales per row
+                        copy4((lane & 1) ? zero : xsb + step * 8 + xso[i], to);
+                }
+            } else {
+                const int i = c - kXPer - kWPer - kXsPer;
+                const uint32_t to =
+                    stage + kXBytes + kWBytes + kXScale + (wave + i * kWaves) % (kWsIns > 0 ? kWsIns : 1) * 256;
+                if (WHOLE)
+                    copy4(wsb + step * 8, wso[i], to);
+                else
+                    copy4((lane & 1) ? zero : wsb + step * 8 + wso[i], to);
+            }
+        }
+
+        __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
+            return lds_read<i32x4>(stage + xr + half[s] + i * WM * 16 * kStepBytes);
+        }
+        __device__ __forceinline__ i32x4 w(uint32_t stage, int j, int s) const {
+            if constexpr (WTR) return read_tr<BN>(stage + kXBytes, wave % WN * NT + j, s);
+            return lds_read<i32x4>(stage + wr + half[s] + j * 16 * kStepBytes);
+        }
+        __device__ __forceinline__ float x_scale(uint32_t stage, int i) const {
+            return lds_read<float>(stage + kXBytes + kWBytes + ((wave / WN + i * WM) * 16 + (lane & 15)) * 4);
+        }
+        // the f-th read of half s: the weights' fragments (and scales), then the rows'
+        __device__ __forceinline__ void read(Frags &h, uint32_t stage, int f, int s) const {
+            if constexpr (FORM == kMx4) {
+                const uint32_t at = stage + kXBytes + kWBytes + (lane & 15) * 8 + (lane >> 4) * 2 + s;
+                const int i = f / 2;
+                if (f % 2 == 0 && i < NT) h.w[i] = w(stage, i, s);
+                if (f % 2 == 1 && i < NT) h.ws[i] = lds_read<uint8_t>(at + kXScale + (wave % WN * NT + i) * 128);
+                if (f % 2 == 0 && i >= NT) h.x[i - NT] = x(stage, i - NT, s);
+                if (f % 2 == 1 && i >= NT) h.xs[i - NT] = lds_read<uint8_t>(at + (wave / WN + (i - NT) * WM) * 128);
+            } else {
+                if (f < NT)
+                    h.w[f] = w(stage, f, s);
+                else
+                    h.x[f - NT] = x(stage, f - NT, s);
+            }
+        }
+        __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
+            if constexpr (FORM == kMx4)
+                mfma_mx4<kAcc>(h.w[j], h.x[i], c, h.ws[j], h.xs[i]);
+            else
+                mfma_bf16<kAcc>(h.w[j], h.x[i], c);
+        }
+    };
+
+    template <int ACT>
+    static __device__ __forceinline__ void tile(const ProductArgs &a, const Shared &sh, uint32_t ring, int wave,
+                                                int lane, int e, int n0, int rows) {
+        const int wm = wave / WN, wn = wave % WN;
+        f32x4 acc[ACT][NTILES];
+#pragma unroll
+        for (int i = 0; i < ACT; ++i)
+#pragma unroll
+            for (int j = 0; j < NTILES; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        const Tile<ACT> t(a, sh, wave, lane, e, n0);
+        if constexpr (FORM == kFp8) {
+            static_assert(128 % (NTILES * 16) == 0, "a wave's channels share one weight scale");
+            const int nb = min(n0 + wn * NTILES * 16, a.N - 1) / 128;
+            reduce_fp8(t, ring, a.steps,
+                       (constant_f32)(uintptr_t)a.w_scales + ((int64_t)e * ((a.N + 127) / 128) + nb) * (a.K / 128), acc);
+        } else {
+            reduce(t, ring, a.steps, t.row_bytes / kStepBytes, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < ACT; ++i) {
+            const int m = (wm + i * WM) * 16 + (lane & 15);
+            if (m >= rows) continue;
+            uint16_t *o = a.out + (int64_t)sh.row[m] * a.N;
+#pragma unroll
+            for (int j = 0; j < NTILES; ++j) {
+                const int n = n0 + (wn * NTILES + j) * 16 + (lane >> 4) * 4;
+                if (n < a.N)
+                    *(u16x4 *)(o + n) =
+                        u16x4{bf16_of(acc[i][j].x), bf16_of(acc[i][j].y), bf16_of(acc[i][j].z), bf16_of(acc[i][j].w)};
             }
         }
     }
 
-    template <int ACT>
-    static __device__ __forceinline__ void reduce(const ProductArgs &a, const Sources &src, uint32_t ring, int wave,
-                                                  int lane, int n0, constant_f32 w_scale_row, f32x4 (&acc)[MT][NT]) {
-        const int wm = wave / WN, wn = wave % WN;
+    // Tile height: the counts are known here only. The fewest rounds of the
+    // grid, each as long as its tiles are high (and some 96 rows' time more,
+    // for what a tile costs whatever its height): a batch whose rows are few,
+    // or all on one expert, gets lower tiles on more compute units.
+    static __device__ __forceinline__ int choose_height(const ProductArgs &a, Shared &sh, int ntiles) {
+        const int tid = threadIdx.x;
+        if (tid < 3) sh.tiles[tid] = 0;
+        __syncthreads();
+        int t[3] = {0, 0, 0};
+        for (int e = tid; e < a.g.E; e += kThreads) {
+            const int c = ep::group_count(a.g, e);
+            sh.ends[e] = c;
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i)
-            if (i < a.steps) copy_step(a, src, ring + i * kStage, i, wave, lane, n0);
-        int slot = 0, fill = STAGES - 1;
-        float next_scale = FORM == kFp8 ? w_scale_row[0] : 1.0f;
-        for (int step = 0; step < a.steps; ++step) {
-            if (STAGES > 2 && step + STAGES - 2 < a.steps)
-                wait_copies<(STAGES - 2) * kPer>();
-            else
-                wait_copies<0>();
-            if (step + STAGES - 1 < a.steps)
-                copy_step(a, src, ring + fill * kStage, step + STAGES - 1, wave, lane, n0);
-            const float w_scale = next_scale;
-            if constexpr (FORM == kFp8) next_scale = w_scale_row[step + 1 < a.steps ? step + 1 : step];
-            multiply<ACT>(ring + slot * kStage, w_scale, wm, wn, lane, acc);
-            slot = slot + 1 == STAGES ? 0 : slot + 1;
-            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            for (int i = 0; i < 3; ++i) t[i] = ep::group_add(t[i], (int)(((int64_t)c + (MOST >> i) - 1) / (MOST >> i)));
         }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (t[i]) atomicAdd(&sh.tiles[i], t[i]);
+        __syncthreads();
+        int best = MOST;
+        int64_t least = INT64_MAX;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int64_t rounds = ((int64_t)sh.tiles[i] * ntiles + gridDim.x - 1) / gridDim.x;
+            const int64_t cost = rounds * ((MOST >> i) + 96);
+            if (cost < least) least = cost, best = MOST >> i;
+        }
+        for (int e = tid; e < a.g.E; e += kThreads) sh.ends[e] = (int)(((int64_t)sh.ends[e] + best - 1) / best);
+        ep::group_prefix(sh.ends, a.g.E);
+        return __builtin_amdgcn_readfirstlane(best);
     }
 
     static __device__ __forceinline__ void body(const ProductArgs &a, Shared &sh) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int wm = wave / WN, wn = wave % WN;
-        const uint32_t ring = lds_address(&sh.ring[0][0]);
+        const uint32_t ring = lds_address(sh.ring);
         const int ntiles = (a.N + BN - 1) / BN;
-        const int mtiles = ep::group_scan(a.g, BM, sh.ends, kThreads);
-        const int64_t tiles = (int64_t)mtiles * ntiles;
+        const int bm = choose_height(a, sh, ntiles);
+        const int64_t tiles = (int64_t)sh.ends[a.g.E - 1] * ntiles;
         // workgroups of one XCD (block index mod 8) take neighbouring tiles: they share rows and weights in its L2
         const int grid = gridDim.x;
         const int first = grid % 8 == 0 ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
         for (int64_t t = first; t < tiles; t += grid) {
-            // expert, then groups of up to 8 row tiles, within one the row tiles first
+            // expert, then bands of up to 8 row tiles, within one the row tiles first
             const int e = __builtin_amdgcn_readfirstlane(ep::group_find(sh.ends, a.g.E, (int)(t / ntiles)));
             const int et0 = __builtin_amdgcn_readfirstlane(e ? sh.ends[e - 1] : 0);
             const int em = __builtin_amdgcn_readfirstlane(sh.ends[e]) - et0;
             const int64_t lt = t - (int64_t)et0 * ntiles;
             const int band = (int)(lt / (8 * ntiles));
             const int inb = (int)(lt - (int64_t)band * 8 * ntiles);
-            const int bm = min(8, em - band * 8);
-            const int m0 = (band * 8 + inb % bm) * BM, n0 = inb / bm * BN;
-            const int rows = __builtin_amdgcn_readfirstlane(ep::group_count(a.g, e)) - m0;  // > 0 unless the counts overflowed the scan
-            if (rows <= 0) continue;
-            __syncthreads();  // the last tile's reads of the ring and the row list are done
-            for (int i = tid; i < BM; i += kThreads)
+            const int high = min(8, em - band * 8);
+            const int m0 = (band * 8 + inb % high) * bm, n0 = inb / high * BN;
+            const int rows = min(__builtin_amdgcn_readfirstlane(ep::group_count(a.g, e)) - m0, bm);
+            if (rows <= 0) continue;  // the counts overflowed the scan
+            __syncthreads();          // the last tile's reads of the ring and the row list are done
+            for (int i = tid; i < MOST; i += kThreads)
                 sh.row[i] = (int)ep::group_row(a.g, e, m0 + (i < rows ? i : rows - 1));
             __syncthreads();
-
-            Sources src;
-            const int64_t xb = FORM == kBf16 ? (int64_t)a.K * 2 : FORM == kFp8 ? a.K : a.K / 2;
-            const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-#pragma unroll
-            for (int i = 0; i < kXPer; ++i) src.x[i] = a.x + sh.row[x_ins(wave, i) * 8 + (lane >> 3)] * xb + chunk;
-#pragma unroll
-            for (int i = 0; i < kWPer; ++i) {
-                if (WTR) {  // W[e] is [K reduction rows][N columns]; columns past the end repeat the last chunk
-                    const int at = w_ins(wave, i) * 64 + lane, r = at / (BN / 8), pc = at % (BN / 8);
-                    const int n = n0 + ((((pc >> 1) ^ tr_swizzle(r)) << 1) | (pc & 1)) * 8;
-                    src.w[i] = a.w + (((int64_t)e * a.K + r) * a.N + min(n, a.N - 8)) * 2;
-                } else {  // rows past the end repeat the last one
-                    const int n = min(n0 + w_ins(wave, i) * 8 + (lane >> 3), a.N - 1);
-                    src.w[i] = a.w + ((int64_t)e * a.N + n) * xb + chunk;
-                }
-            }
-            if constexpr (FORM == kFp8) {
-#pragma unroll
-                for (int i = 0; i < kXsPer; ++i)
-                    src.xs[i] = a.x_scales +
-                                (int64_t)sh.row[min(((wave + i * kWaves) % kXsIns) * 64 + lane, BM - 1)] * (a.K / 128) * 4;
-            }
-            if constexpr (FORM == kMx4) {
-#pragma unroll
-                for (int i = 0; i < kXsPer; ++i)
-                    src.xs[i] = a.x_scales +
-                                (int64_t)sh.row[min(((wave + i * kWaves) % kXsIns) * 32 + (lane >> 1), BM - 1)] * (a.K / 32) +
-                                (lane & 1) * 4;
-#pragma unroll
-                for (int i = 0; i < kWsPer; ++i) {
-                    const int n = min(n0 + ((wave + i * kWaves) % kWsIns) * 32 + (lane >> 1), a.N - 1);
-                    src.ws[i] = a.w_scales + ((int64_t)e * a.N + n) * (a.K / 32) + (lane & 1) * 4;
-                }
-            }
-            constant_f32 w_scale_row = nullptr;
-            if constexpr (FORM == kFp8) {
-                static_assert(FORM != kFp8 || 128 % (NT * 16) == 0, "a wave's channels share one weight scale");
-                const int nb = min(n0 + wn * NT * 16, a.N - 1) / 128;
-                w_scale_row = (constant_f32)(uintptr_t)a.w_scales + ((int64_t)e * ((a.N + 127) / 128) + nb) * (a.K / 128);
-            }
-
-            f32x4 acc[MT][NT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-            // row tiles are dealt to the waves in turn: a tile with few rows costs each of them less
-            const int act = (min(rows, BM) + 16 * WM - 1) / (16 * WM);
-            if (MT >= 4 && act <= MT / 4)
-                reduce<MT / 4 ? MT / 4 : 1>(a, src, ring, wave, lane, n0, w_scale_row, acc);
+            const int act = (rows + 16 * WM - 1) / (16 * WM);
+            if (MT >= 8 && act <= MT / 8)
+                tile<MT / 8 ? MT / 8 : 1>(a, sh, ring, wave, lane, e, n0, rows);
+            else if (MT >= 4 && act <= MT / 4)
+                tile<MT / 4 ? MT / 4 : 1>(a, sh, ring, wave, lane, e, n0, rows);
             else if (MT >= 2 && act <= MT / 2)
-                reduce<MT / 2 ? MT / 2 : 1>(a, src, ring, wave, lane, n0, w_scale_row, acc);
+                tile<MT / 2 ? MT / 2 : 1>(a, sh, ring, wave, lane, e, n0, rows);
             else
-                reduce<MT>(a, src, ring, wave, lane, n0, w_scale_row, acc);
-
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int m = (wm + i * WM) * 16 + (lane & 15);
-                if (m >= rows) continue;
-                uint16_t *o = a.out + (int64_t)sh.row[m] * a.N;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int n = n0 + (wn * NT + j) * 16 + (lane >> 4) * 4;
-                    if (n < a.N)
-                        *(u16x4 *)(o + n) = u16x4{bf16_of(acc[i][j].x), bf16_of(acc[i][j].y), bf16_of(acc[i][j].z),
-                                                  bf16_of(acc[i][j].w)};
-                }
-            }
+                tile<MT>(a, sh, ring, wave, lane, e, n0, rows);
         }
     }
 };
 
-template <int FORM, bool WTR, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM *WN * 64) void k_product(ProductArgs a) {
-    using P = Product<FORM, WTR, BM, BN, WM, WN, STAGES>;
+template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
+__global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_product(ProductArgs a) {
+    using P = Product<FORM, WTR, BN, WM, WN, MT>;
     __shared__ typename P::Shared sh;
     P::body(a, sh);
 }
-
 
 // ---------------------------------------------------------------------------
 // wgrad
@@ -427,39 +659,85 @@ struct WgradArgs {
 // read through the transposing read. A BM (n) x BN (k) tile, 64 rows a step;
 // rows past the expert's last are zeros on both sides, so that whatever the
 // unused receive rows hold (NaN included) does not enter a sum.
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int WM, int WN>
 struct Wgrad {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-    static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;
-    static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes;
+    static constexpr int ACT = BM / 16 / WM, NT = BN / 16 / WN;
+    static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes, kStages = 2;
     static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + kXPer;
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
+    using Frags = HalfFrags<ACT, NT, false>;
+    static constexpr int kReads = ACT + NT;
+    static constexpr bool kAcc = ACT * NT >= 64;
 
     struct Shared {
-        uint8_t ring[STAGES][kStage];
+        uint8_t ring[kStages * kStage];
     };
 
-    template <int COLS, int PER>
-    static __device__ __forceinline__ void copy_side(const WgradArgs &a, const uint8_t *rows, int width, int c0, int e,
-                                                     int64_t base, int count, int step, uint32_t tile, int wave,
-                                                     int lane) {
+    const GroupArgs *g;
+    const uint8_t *gb, *xb;  // bases: packed layout, the expert's first row; low-latency, the arrays
+    uint32_t go[kGPer], xo[kXPer];
+    int e, count, wave, lane, grow, xrow;  // rows' bytes
+
+    __device__ __forceinline__ Wgrad(const WgradArgs &a, int e_, int count_, int n0, int k0, int wave_, int lane_)
+        : g(&a.g), e(e_), count(count_), wave(wave_), lane(lane_), grow(a.N * 2), xrow(a.K * 2) {
+        const int64_t base = a.g.region_rows > 0 || count == 0 ? 0 : ep::group_row(a.g, e, 0);
+        gb = uniform(a.grad + base * grow + n0 * 2);
+        xb = uniform(a.x + base * xrow + k0 * 2);
+        // columns past the end repeat the last chunk
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int ins = wave + i * kWaves;
-            const int at = ins * 64 + lane, r = at / (COLS / 8), pc = at % (COLS / 8);
-            const int c = min(c0 + ((((pc >> 1) ^ tr_swizzle(r)) << 1) | (pc & 1)) * 8, width - 8);
-            const int m = step * 64 + r;
-            const uint8_t *p = (const uint8_t *)&k_zero_chunk;
-            if (m < count) p = rows + ((a.g.region_rows > 0 ? ep::group_row(a.g, e, m) : base + m) * width + c) * 2;
-            copy16(p, tile + ins * 1024);
+        for (int i = 0; i < kGPer; ++i) {
+            int r, c;
+            tr_place<BM>(wave + i * kWaves, lane, r, c);
+            go[i] = (uint32_t)r * grow + min(c, a.N - 8 - n0) * 2;
         }
+#pragma unroll
+        for (int i = 0; i < kXPer; ++i) {
+            int r, c;
+            tr_place<BN>(wave + i * kWaves, lane, r, c);
+            xo[i] = (uint32_t)r * xrow + min(c, a.K - 8 - k0) * 2;
+        }
+    }
+
+    template <bool WHOLE>
+    __device__ __forceinline__ void copy(int step, uint32_t stage, int c) const {
+        const bool of_grad = c < kGPer;
+        const int ins = wave + (of_grad ? c : c - kGPer) * kWaves;
+        const uint32_t to = stage + (of_grad ? 0 : kGBytes) + ins * 1024;
+        const int width = of_grad ? grow : xrow;
+        const uint8_t *base = of_grad ? gb : xb;
+        const uint32_t off = of_grad ? go[c < kGPer ? c : 0] : xo[c < kGPer ? 0 : c - kGPer];
+        if (WHOLE) {  // packed layout, all rows the expert's
+            copy16(base + (int64_t)step * 64 * width, off, to);
+            return;
+        }
+        const int r = (ins * 64 + lane) / ((of_grad ? BM : BN) / 8), m = step * 64 + r;
+        const uint8_t *p = (const uint8_t *)&k_zero_chunk;
+        if (m < count)
+            p = g->region_rows > 0 ? base + ep::group_row(*g, e, m) * width + (off - (uint32_t)r * width)
+                                   : base + (int64_t)step * 64 * width + off;
+        copy16(p, to);
+    }
+    __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
+        return read_tr<BM>(stage, wave / WN + i * WM, s);
+    }
+    __device__ __forceinline__ i32x4 w(uint32_t stage, int j, int s) const {
+        return read_tr<BN>(stage + kGBytes, wave % WN * NT + j, s);
+    }
+    __device__ __forceinline__ void read(Frags &h, uint32_t stage, int f, int s) const {
+        if (f < NT)
+            h.w[f] = w(stage, f, s);
+        else
+            h.x[f - NT] = x(stage, f - NT, s);
+    }
+    __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
+        mfma_bf16<kAcc>(h.w[j], h.x[i], c);
     }
 
     static __device__ __forceinline__ void body(const WgradArgs &a, Shared &sh) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WN, wn = wave % WN;
-        const uint32_t ring = lds_address(&sh.ring[0][0]);
         const int nt = (a.N + BM - 1) / BM, kt = (a.K + BN - 1) / BN;
         const int64_t tiles = (int64_t)a.g.E * nt * kt;
         const int grid = gridDim.x;
@@ -467,54 +745,23 @@ struct Wgrad {
         for (int64_t t = first; t < tiles; t += grid) {
             const int e = __builtin_amdgcn_readfirstlane((int)(t / (nt * kt)));
             const int lt = __builtin_amdgcn_readfirstlane((int)(t - (int64_t)e * nt * kt));
-            const int band = lt / (8 * kt), inb = lt - band * 8 * kt, bm = min(8, nt - band * 8);
-            const int n0 = (band * 8 + inb % bm) * BM, k0 = inb / bm * BN;
+            const int band = lt / (8 * kt), inb = lt - band * 8 * kt, high = min(8, nt - band * 8);
+            const int n0 = (band * 8 + inb % high) * BM, k0 = inb / high * BN;
             const int count = __builtin_amdgcn_readfirstlane(ep::group_count(a.g, e));
-            const int64_t base = a.g.region_rows > 0 || count == 0
-                                     ? 0
-                                     : (int64_t)(e / a.g.epr) * a.g.cap_rows + a.g.offsets[e];
-            const int steps = (count + 63) / 64;
-            __syncthreads();  // the last tile's reads of the ring are done
-
-            f32x4 acc[MT][NT];
+            f32x4 acc[ACT][NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < ACT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-            auto copy_step = [&](int step, int slot) {
-                const uint32_t st = ring + slot * kStage;
-                copy_side<BM, kGPer>(a, a.grad, a.N, n0, e, base, count, step, st, wave, lane);
-                copy_side<BN, kXPer>(a, a.x, a.K, k0, e, base, count, step, st + kGBytes, wave, lane);
-            };
-#pragma unroll
-            for (int i = 0; i < STAGES - 1; ++i)
-                if (i < steps) copy_step(i, i);
-            int slot = 0, fill = STAGES - 1;
-            for (int step = 0; step < steps; ++step) {
-                if (STAGES > 2 && step + STAGES - 2 < steps)
-                    wait_copies<(STAGES - 2) * kPer>();
-                else
-                    wait_copies<0>();
-                if (step + STAGES - 1 < steps) copy_step(step + STAGES - 1, fill);
-                const uint32_t st = ring + slot * kStage;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    i32x4 xf[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) xf[j] = read_tr<BN>(st + kGBytes, wn * NT + j, s);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const i32x4 gf = read_tr<BM>(st, wm + i * WM, s);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) acc[i][j] = mfma_bf16(xf[j], gf, acc[i][j]);
-                    }
-                }
-                slot = slot + 1 == STAGES ? 0 : slot + 1;
-                fill = fill + 1 == STAGES ? 0 : fill + 1;
+            if (count > 0) {
+                __syncthreads();  // the last tile's reads of the ring are done
+                reduce(Wgrad(a, e, count, n0, k0, wave, lane), lds_address(sh.ring), (count + 63) / 64,
+                       a.g.region_rows > 0 ? 0 : count / 64, acc);
+            } else if (a.accumulate) {
+                continue;
             }
-
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
+            for (int i = 0; i < ACT; ++i) {
                 const int n = n0 + (wm + i * WM) * 16 + (lane & 15);
                 if (n >= a.N) continue;
                 const int64_t row = ((int64_t)e * a.N + n) * a.K;
@@ -535,9 +782,9 @@ struct Wgrad {
     }
 };
 
-template <int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM *WN * 64) void k_wgrad(WgradArgs a) {
-    using P = Wgrad<BM, BN, WM, WN, STAGES>;
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_wgrad(WgradArgs a) {
+    using P = Wgrad<BM, BN, WM, WN>;
     __shared__ typename P::Shared sh;
     P::body(a, sh);
 }
@@ -548,34 +795,28 @@ __global__ __launch_bounds__(WM *WN * 64) void k_wgrad(WgradArgs a) {
 
 // A launch fills the chip with as many workgroups as it holds at once (they
 // loop over the tiles), or fewer where there cannot be that many tiles.
-template <int FORM, bool WTR, int BM, int BN, int WM, int WN, int STAGES>
-hipError_t launch_product(const ProductArgs &a, int64_t rows, int cus, hipStream_t s) {
-    using P = Product<FORM, WTR, BM, BN, WM, WN, STAGES>;
-    constexpr int kPerCu = sizeof(typename P::Shared) * 2 <= 160 * 1024 ? 2 : 1;
-    const int64_t tiles = (rows / BM + a.g.E) * ((a.N + BN - 1) / BN);
-    const int grid = (int)(tiles < (int64_t)cus * kPerCu ? tiles : (int64_t)cus * kPerCu);
-    k_product<FORM, WTR, BM, BN, WM, WN, STAGES><<<grid, P::kThreads, 0, s>>>(a);
+template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
+hipError_t launch_product(const ProductArgs &a, int grid, hipStream_t s) {
+    k_product<FORM, WTR, BN, WM, WN, MT><<<grid, WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
-// Row tiles by the rows an expert has on average, rounded up well past it: an
-// expert's weights are read once per row tile, and a row tile with few rows
-// costs only the matrix instructions of the rows it has (in quarters).
+// 256-channel tiles of up to 256 rows where there are enough of them for the
+// chip, else 128-channel tiles of up to 128 rows, two workgroups to a CU.
 template <int FORM, bool WTR>
 hipError_t launch_product_form(const ProductArgs &a, int64_t rows, int cus, hipStream_t s) {
-    const int64_t per = rows / a.g.E;
-    if (per <= 8) return launch_product<FORM, WTR, 16, 128, 1, 4, 4>(a, rows, cus, s);
-    if (per <= 48) return launch_product<FORM, WTR, 64, 128, 1, 4, 3>(a, rows, cus, s);
-    return launch_product<FORM, WTR, 256, 256, 2, 4, 2>(a, rows, cus, s);
+    const int64_t experts = rows < a.g.E ? rows : a.g.E;
+    const int64_t big = (rows / 256 > experts ? rows / 256 : experts) * ((a.N + 255) / 256);
+    if (big >= cus) return launch_product<FORM, WTR, 256, 2, FORM == kFp8 ? 4 : 2, 8>(a, cus, s);
+    const int64_t most = (rows / 32 + experts) * ((a.N + 127) / 128);
+    return launch_product<FORM, WTR, 128, 2, 2, 4>(a, (int)(most < 2 * cus ? most : 2 * cus), s);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int WM, int WN>
 hipError_t launch_wgrad(const WgradArgs &a, int cus, hipStream_t s) {
-    using P = Wgrad<BM, BN, WM, WN, STAGES>;
-    constexpr int kPerCu = sizeof(typename P::Shared) * 2 <= 160 * 1024 ? 2 : 1;
     const int64_t tiles = (int64_t)a.g.E * ((a.N + BM - 1) / BM) * ((a.K + BN - 1) / BN);
-    const int grid = (int)(tiles < (int64_t)cus * kPerCu ? tiles : (int64_t)cus * kPerCu);
-    k_wgrad<BM, BN, WM, WN, STAGES><<<grid, P::kThreads, 0, s>>>(a);
+    const int64_t most = (int64_t)cus * (BN >= 256 ? 1 : 2);
+    k_wgrad<BM, BN, WM, WN><<<(int)(tiles < most ? tiles : most), WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -663,8 +904,8 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     a.out_f32 = out_f32 != 0;
     a.accumulate = accumulate != 0;
     const int64_t big = (int64_t)a.g.E * ((N + 255) / 256) * ((K + 255) / 256);
-    const hipError_t e = big >= cus ? launch_wgrad<256, 256, 2, 4, 2>(a, cus, (hipStream_t)stream)
-                                    : launch_wgrad<128, 128, 2, 2, 2>(a, cus, (hipStream_t)stream);
+    const hipError_t e = big >= cus ? launch_wgrad<256, 256, 2, 2>(a, cus, (hipStream_t)stream)
+                                    : launch_wgrad<128, 128, 2, 2>(a, cus, (hipStream_t)stream);
     return ep::hip_status(e, "ep_expert_gemm_wgrad");
 }
 

@@ -70,28 +70,33 @@ __device__ __forceinline__ int group_add(int a, int b) {
     return s > 0x7FFFFFFFu ? 0x7FFFFFFF : (int)s;
 }
 
-// ends[e] = sum over experts <= e of ceil(count / per) in LDS, by one
-// workgroup of `threads` threads (whole waves); ends with a barrier. Returns
-// the total. E <= kGroupsMaxExperts entries.
-__device__ __forceinline__ int group_scan(const GroupArgs &g, int per, int *ends, int threads) {
+// In place: ends[e] = sum of ends[i], i <= e, by the workgroup's first wave.
+// Between barriers of its own. E <= kGroupsMaxExperts entries in LDS.
+__device__ __forceinline__ void group_prefix(int *ends, int E) {
     const int tid = threadIdx.x;
-    for (int e = tid; e < g.E; e += threads) ends[e] = (group_count(g, e) + per - 1) / per;
     __syncthreads();
     if (tid < 64) {
         int carry = 0;
-        for (int base = 0; base < g.E; base += 64) {
+        for (int base = 0; base < E; base += 64) {
             const int e = base + tid;
-            int v = e < g.E ? ends[e] : 0;
+            int v = e < E ? ends[e] : 0;
             for (int d = 1; d < 64; d <<= 1) {
                 const int u = __shfl_up(v, d);
                 if (tid >= d) v = group_add(v, u);
             }
             v = group_add(v, carry);
-            if (e < g.E) ends[e] = v;
+            if (e < E) ends[e] = v;
             carry = __shfl(v, 63);
         }
     }
     __syncthreads();
+}
+
+// ends[e] = rows of the experts <= e, by a workgroup of `threads` threads
+// (whole waves). Returns all rows.
+__device__ __forceinline__ int group_scan(const GroupArgs &g, int *ends, int threads) {
+    for (int e = threadIdx.x; e < g.E; e += threads) ends[e] = group_count(g, e);
+    group_prefix(ends, g.E);
     return ends[g.E - 1];
 }
 

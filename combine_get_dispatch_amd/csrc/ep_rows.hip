@@ -258,7 +258,7 @@ template <int OP>
 __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs a) {
     constexpr int U = Lane<OP>::kUnroll, PER = Lane<OP>::kPer, VECS = OP == kDequantize ? 2 : 2 * Lane<OP>::kVecs + 1;
     __shared__ int ends[ep::kGroupsMaxExperts];
-    const int64_t rows = a.grouped ? ep::group_scan(a.g, 1, ends, kThreads) : a.num_rows;
+    const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
     const int lane = threadIdx.x & 63;
     const int64_t waves = (int64_t)gridDim.x * (kThreads / 64);
     const int64_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
