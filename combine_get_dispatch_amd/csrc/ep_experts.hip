@@ -201,6 +201,7 @@ __device__ __forceinline__ void settle() {
 // The ring's first steps: whole ones, then those with chunks past the end.
 template <class P>
 __device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, int whole) {
+    if (P::kRuns) p.first_run();
 #pragma unroll
     for (int i = 0; i < P::kStages; ++i) {
         if (i < whole) {
@@ -236,7 +237,7 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
         wait_copies<0>();
     typename P::Frags h0, h1;
 #pragma unroll
-    for (int f = 0; f < P::kReads; ++f) p.read(h0, ring, f, 0);
+    for (int f = 0; f < P::kReads; ++f) p.read(h0, ring, 0, f, 0);
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
@@ -247,7 +248,7 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
 #pragma unroll
         for (int m = 0; m < M; ++m) {
 #pragma unroll
-            for (int f = m * I1 / M; f < (m + 1) * I1 / M; ++f) p.read(h1, st, f, 1);
+            for (int f = m * I1 / M; f < (m + 1) * I1 / M; ++f) p.read(h1, st, step, f, 1);
             p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
@@ -261,7 +262,7 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
                 if (COPIES != kNone && (f + 1) * P::kPer / I2 > c)
                     p.template copy<COPIES == kWhole>(step + S, st, c);
                 else
-                    p.read(h0, nx, COPIES != kNone ? f - c : f, 0);
+                    p.read(h0, nx, step + 1, COPIES != kNone ? f - c : f, 0);
             }
             p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
@@ -270,72 +271,95 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
         ++step;
     };
     while (step + S < whole) body(std::integral_constant<int, kWhole>());
-    while (step + S < steps) body(std::integral_constant<int, kPartial>());
+    if (!P::kRuns)  // with runs of scales all steps are whole
+        while (step + S < steps) body(std::integral_constant<int, kPartial>());
     while (step < steps) body(std::integral_constant<int, kNone>());
 }
 
 // The FP8 form's reduction: a step is one block of 128 channels, its products
 // of a row tile summed by one matrix instruction from zero and added times
-// the row's and the weights' scale. Fragments are read two row tiles ahead
-// and added one row tile behind. (K is a multiple of 128: all steps are whole.)
+// the row's and the weights' scale. A row tile's sums are added while the
+// next row tile's matrix instructions run, four additions behind each; the
+// next fragments are read meanwhile, at the step's last row tile those of the
+// next step. (K is a multiple of 128: all steps are whole.)
 template <class P>
 __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps, constant_f32 w_scales,
                                            f32x4 (&acc)[P::ACT][P::NT]) {
     constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
+    static_assert(ACT == 1 || ACT % 2 == 0, "row tiles alternate between two registers");
     fill_ring(p, ring, steps, steps);
-    int slot = 0, step = 0;
+    if (S <= steps)
+        wait_copies<(S - 1) * P::kPer>();
+    else
+        wait_copies<0>();
+    i32x8 w[NT], x[2];
+    f32x4 part[2][NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        w[j] = join(p.w(ring, j, 0), p.w(ring, j, 1));
+        part[1][j] = f32x4{0, 0, 0, 0};
+    }
+    x[0] = join(p.x(ring, 0, 0), p.x(ring, 0, 1));
+    float s_next = p.x_scale(ring, 0, 0), f = 0.0f, f_prev = 0.0f;  // times 0: there is no tile before the first
     float ws = w_scales[0];
+    int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
-        wait_copies<(COPIES == kNone ? 0 : (S - 1) * P::kPer)>();
         const uint32_t st = ring + slot * P::kStage;
         slot = slot + 1 == S ? 0 : slot + 1;
-        i32x8 w[NT], x[3];
-        float s[4];  // one more than the fragments: used a row tile later
-        f32x4 part[2][NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) w[j] = join(p.w(st, j, 0), p.w(st, j, 1));
-#pragma unroll
-        for (int i = 0; i < (ACT < 2 ? ACT : 2); ++i) {
-            x[i] = join(p.x(st, i, 0), p.x(st, i, 1));
-            s[i] = p.x_scale(st, i);
-        }
-        pin();
+        const uint32_t nx = ring + slot * P::kStage;
+        const float ws_next = w_scales[step + 1 < steps ? step + 1 : step];
 #pragma unroll
         for (int i = 0; i < ACT; ++i) {
-            if (i + 2 < ACT) {
-                x[(i + 2) % 3] = join(p.x(st, i + 2, 0), p.x(st, i + 2, 1));
-                s[(i + 2) % 4] = p.x_scale(st, i + 2);
+            const bool last = i == ACT - 1;
+            if (last) {  // the step's buffer has been read out, the next one's must have landed
+                wait_copies<(COPIES == kNone ? 0 : (S - 2) * P::kPer)>();
+            }
+            f_prev = f;
+            f = s_next * ws;
+            if (!last) {
+                x[(i + 1) & 1] = join(p.x(st, i + 1, 0), p.x(st, i + 1, 1));
+                s_next = p.x_scale(st, step, i + 1);
+            } else {
+                s_next = p.x_scale(nx, step + 1, 0);
+                if (ACT > 1) x[0] = join(p.x(nx, 0, 0), p.x(nx, 0, 1));
             }
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j) {
+                const f32x4 before = part[(i + 1) & 1][j];
                 part[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    w[j], x[i % 3], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-            if (i > 0) {
-                const float f = s[(i - 1) % 4] * ws;
+                    w[j], x[i & 1], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                if (last) {
+                    if (COPIES != kNone) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                        for (int c = j * P::kPer / NT; c < (j + 1) * P::kPer / NT; ++c)
+                            p.template copy<true>(step + S, st, c);
+                    }
+                    w[j] = join(p.w(nx, j, 0), p.w(nx, j, 1));
+                }
+                const int to = (i + ACT - 1) % ACT;
+                if (ACT > 1) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i - 1][j][q] = fmaf(part[(i - 1) & 1][j][q], f, acc[i - 1][j][q]);
+                    for (int q = 0; q < 4; ++q) acc[to][j][q] = fmaf(before[q], f_prev, acc[to][j][q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[0][j][q] = fmaf(part[0][j][q], f, acc[0][j][q]);
+                }
+                pin();
             }
-            pin();
+            if (ACT == 1) x[0] = join(p.x(nx, 0, 0), p.x(nx, 0, 1));
         }
-        const float f = s[(ACT - 1) % 4] * ws;
-        ws = w_scales[step + 1 < steps ? step + 1 : step];
-        if (COPIES != kNone) {
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffer has been read out
-#pragma unroll
-            for (int c = 0; c < P::kPer; ++c) p.template copy<true>(step + S, st, c);
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                acc[ACT - 1][j][q] = fmaf(part[(ACT - 1) & 1][j][q], f, acc[ACT - 1][j][q]);
+        ws = ws_next;
         ++step;
     };
     while (step + S < steps) body(std::integral_constant<int, kWhole>());
     while (step < steps) body(std::integral_constant<int, kNone>());
+    if (ACT > 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[ACT - 1][j][q] = fmaf(part[1][j][q], f, acc[ACT - 1][j][q]);
+    }
 }
 
 // One half's fragments: weights' side, rows' side, MXFP4 scales of both.
@@ -353,16 +377,29 @@ struct HalfFrags {
 // WN waves. Row tiles of 16 are dealt to the WM waves in turn, so that a tile
 // with few rows costs each of them as little, in steps of half, a quarter, an
 // eighth (ACT row tiles per wave), of rows copied as well as multiplied.
-template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
+//
+// Scales are copied in runs of several steps, 16 or 32 bytes per row, where
+// their rows allow it (RUNS: K % 512 == 0): a copy instruction takes a cycle
+// or more per memory line its lanes touch, and every row of the scales is
+// another line. (Step by step they cost 12% of a 256 x 256 tile's time.)
+template <int FORM, bool WTR, int BN, int WM, int WN, int MT, bool RUNS>
 struct Product {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int MOST = 16 * WM * MT, NTILES = BN / 16 / WN;
     static constexpr bool kAccumulate = MT * NTILES >= 64;  // 256 accumulators a lane: all registers of a SIMD
-    static constexpr int kRing = BN >= 256 ? 144 * 1024 : 72 * 1024;
+    static constexpr bool kScaled = FORM != kBf16;
+    // steps per run of scales, and the runs' bytes (three in LDS: one read, one or two on their way)
+    static constexpr int kRun = FORM == kFp8 ? 4 : 2, kXsRun = RUNS ? MOST * 16 : 0;
+    static constexpr int kWsRun = RUNS && FORM == kMx4 ? BN * 16 : 0;
+    static constexpr int kRing = (BN >= 256 ? (!RUNS ? 144 : FORM == kMx4 ? 128 : 136) : RUNS ? 64 : 72) * 1024;
+    static constexpr int kMaxStages = RUNS ? 3 : 4;
+    static_assert(!RUNS || (FORM == kFp8 && MOST == 32 * kWaves) || (FORM == kMx4 && MOST == 64 * kWaves && BN == MOST),
+                  "who copies which rows' scales");
     static_assert(!WTR || FORM == kBf16, "only bf16 has a transposing read");
 
     struct Shared {
         uint8_t ring[kRing];
+        uint8_t scales[RUNS ? 3 * (kXsRun + kWsRun) : 16];
         int ends[ep::kGroupsMaxExperts];
         int row[MOST];
         int tiles[3];
@@ -373,18 +410,19 @@ struct Product {
     struct Tile {
         static constexpr int ACT = ACT_, NT = NTILES, ROWS = 16 * WM * ACT;
         static constexpr int kXBytes = ROWS * kStepBytes, kWBytes = BN * kStepBytes;
-        // scales of one step: FP8 one float per row; MX4 eight bytes per row of both sides
-        static constexpr int kXScale = FORM == kFp8 ? (ROWS < 64 ? 64 : ROWS) * 4 : FORM == kMx4 ? ROWS * 8 : 0;
-        static constexpr int kWScale = FORM == kMx4 ? BN * 8 : 0;
+        // single steps' scales follow the tiles: FP8 one float per row; MX4 eight bytes per row of both sides
+        static constexpr bool kRuns = RUNS, kSingle = kScaled && !RUNS;
+        static constexpr int kXScale = !kSingle ? 0 : FORM == kFp8 ? (ROWS < 64 ? 64 : ROWS) * 4 : ROWS * 8;
+        static constexpr int kWScale = kSingle && FORM == kMx4 ? BN * 8 : 0;
         static constexpr int kStage = kXBytes + kWBytes + kXScale + kWScale;
-        static constexpr int kStages = kRing / kStage < 4 ? kRing / kStage : 4;
+        static constexpr int kStages = kRing / kStage < kMaxStages ? kRing / kStage : kMaxStages;
         // copies per step; every wave issues as many (some repeat another's), so that one count of copies in flight
         // holds for each
         static constexpr int kXIns = kXBytes / 1024, kWIns = kWBytes / 1024;
         static constexpr int kXPer = (kXIns + kWaves - 1) / kWaves, kWPer = (kWIns + kWaves - 1) / kWaves;
         static constexpr int kXsIns = kXScale / 256, kWsIns = kWScale / 256;
         static constexpr int kXsPer = (kXsIns + kWaves - 1) / kWaves, kWsPer = (kWsIns + kWaves - 1) / kWaves;
-        static constexpr int kPer = kXPer + kWPer + kXsPer + kWsPer;
+        static constexpr int kPer = kXPer + kWPer + (RUNS ? 1 : kXsPer + kWsPer);
         static_assert(kStages >= 2 && kPer * (kStages - 1) < 64, "ring");
         using Frags = HalfFrags<ACT, NT, FORM == kMx4>;
         static constexpr int kReads = (FORM == kMx4 ? 2 : 1) * (ACT + NT);
@@ -392,7 +430,8 @@ struct Product {
 
         // sources: one base per operand, offsets within the tile per lane
         const uint8_t *xb, *wb, *xsb, *wsb;
-        uint32_t xo[kXPer], wo[kWPer], xso[kXsPer > 0 ? kXsPer : 1], wso[kWsPer > 0 ? kWsPer : 1];
+        uint32_t xo[kXPer], wo[kWPer], xso[RUNS ? 2 : kXsPer > 0 ? kXsPer : 1], wso[kWsPer > 0 ? kWsPer : 1];
+        uint32_t scales;  // the runs, in LDS
         int64_t wstep;   // bytes of the weights' base per step
         int row_bytes;   // of a reduction-contiguous row
         int wave, lane, K;
@@ -401,6 +440,7 @@ struct Product {
 
         __device__ __forceinline__ Tile(const ProductArgs &a, const Shared &sh, int wave_, int lane_, int e, int n0)
             : wave(wave_), lane(lane_), K(a.K) {
+            scales = lds_address(sh.scales);
             const int64_t row0 = __builtin_amdgcn_readfirstlane(sh.row[0]);
             row_bytes = FORM == kBf16 ? a.K * 2 : FORM == kFp8 ? a.K : a.K / 2;
             xb = uniform(a.x + row0 * row_bytes);
@@ -427,24 +467,34 @@ struct Product {
                 }
             }
             xsb = wsb = nullptr;
-            if constexpr (FORM == kFp8) {
-                xsb = uniform(a.x_scales + row0 * (a.K / 128) * 4);
+            if constexpr (kScaled) {
+                const int sb = FORM == kFp8 ? a.K / 128 * 4 : a.K / 32;  // bytes of a row's scales
+                xsb = uniform(a.x_scales + row0 * sb);
+                if constexpr (FORM == kMx4) wsb = uniform(a.w_scales + ((int64_t)e * a.N + n0) * sb);
+                if constexpr (RUNS && FORM == kFp8) {  // 16 rows of 16 bytes a wave, two turns
 #pragma unroll
-                for (int i = 0; i < kXsPer; ++i)
-                    xso[i] = (uint32_t)(sh.row[min((wave + i * kWaves) % kXsIns * 64 + lane, ROWS - 1)] - (int)row0) *
-                             (a.K / 128) * 4;
-            }
-            if constexpr (FORM == kMx4) {
-                xsb = uniform(a.x_scales + row0 * (a.K / 32));
-                wsb = uniform(a.w_scales + ((int64_t)e * a.N + n0) * (a.K / 32));
+                    for (int i = 0; i < 2; ++i)
+                        xso[i] = (uint32_t)(sh.row[(i * kWaves + wave) * 16 + (lane >> 2)] - (int)row0) * sb + (lane & 3) * 4;
+                } else if constexpr (RUNS) {  // 64 rows of 16 bytes a wave, half the waves each side, two turns
 #pragma unroll
-                for (int i = 0; i < kXsPer; ++i)
-                    xso[i] = (uint32_t)(sh.row[(wave + i * kWaves) % kXsIns * 32 + (lane >> 1)] - (int)row0) * (a.K / 32) +
-                             (lane & 1) * 4;
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = (i * (kWaves / 2) + wave % (kWaves / 2)) * 64 + lane;
+                        xso[i] = (uint32_t)(wave < kWaves / 2 ? sh.row[r] - (int)row0 : min(r, a.N - 1 - n0)) * sb;
+                    }
+                    if (wave >= kWaves / 2) xsb = wsb;
+                } else {
+                    constexpr int kRow = FORM == kFp8 ? 1 : 2;  // words per row and step
 #pragma unroll
-                for (int i = 0; i < kWsPer; ++i)
-                    wso[i] = (uint32_t)min((wave + i * kWaves) % kWsIns * 32 + (lane >> 1), a.N - 1 - n0) * (a.K / 32) +
-                             (lane & 1) * 4;
+                    for (int i = 0; i < kXsPer; ++i) {
+                        const int at = (wave + i * kWaves) % (kXsIns > 0 ? kXsIns : 1) * 64 + lane;
+                        xso[i] = (uint32_t)(sh.row[min(at / kRow, ROWS - 1)] - (int)row0) * sb + at % kRow * 4;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kWsPer; ++i) {
+                        const int at = (wave + i * kWaves) % (kWsIns > 0 ? kWsIns : 1) * 64 + lane;
+                        wso[i] = (uint32_t)min(at / kRow, a.N - 1 - n0) * sb + at % kRow * 4;
+                    }
+                }
             }
             const int g = lane >> 4, r = lane & 15, wm = wave / WN, wn = wave % WN;
             xr = wm * 16 * kStepBytes + r * kStepBytes;
@@ -476,16 +526,17 @@ struct Product {
                     const bool ok = WTR ? step * 64 + (ins * 64 + lane) / (BN / 8) < K : in;
                     copy16(ok ? wb + step * wstep + wo[i] : zero, to);
                 }
+            } else if (RUNS) {  // this step's share of the next run
+                copy_run(step / kRun + 1, step & 1);
             } else if (c < kXPer + kWPer + kXsPer) {
                 const int i = c - kXPer - kWPer;
                 const uint32_t to = stage + kXBytes + kWBytes + (wave + i * kWaves) % (kXsIns > 0 ? kXsIns : 1) * 256;
-                if constexpr (FORM == kFp8) copy4(xsb + step * 4, xso[i], to);
-                if constexpr (FORM == kMx4) {
-                    if (WHOLE)
-                        copy4(xsb + step * 8, xso[i], to);
-                    else  // half a step: one word of four scales per row
-                        copy4((lane & 1) ? zero : xsb + step * 8 + xso[i], to);
-                }
+                if (FORM == kFp8)
+                    copy4(xsb + step * 4, xso[i], to);
+                else if (WHOLE)
+                    copy4(xsb + step * 8, xso[i], to);
+                else  // half a step: one word of four scales per row
+                    copy4((lane & 1) ? zero : xsb + step * 8 + xso[i], to);
             } else {
                 const int i = c - kXPer - kWPer - kXsPer;
                 const uint32_t to =
@@ -497,6 +548,21 @@ struct Product {
             }
         }
 
+        // The wave's copy of turn `turn` of run `run` of scales, beside a step of the run before: there when that run's
+        // last step is, and three runs keep clear of the one being read. Past the rows' end the last run again (not read).
+        __device__ __forceinline__ void copy_run(int run, int turn) const {
+            const uint8_t *base = xsb + min(run, row_bytes / (kRun * kStepBytes) - 1) * 16;
+            const uint32_t off = turn ? xso[1] : xso[0], to = scales + run % 3 * (kXsRun + kWsRun);
+            if constexpr (FORM == kFp8)
+                copy4(base, off, to + (turn * kWaves + wave) * 256);
+            else
+                copy16(base, off, to + (wave < kWaves / 2 ? 0 : kXsRun) + (turn * (kWaves / 2) + wave % (kWaves / 2)) * 1024);
+        }
+        __device__ __forceinline__ void first_run() const {
+            copy_run(0, 0);
+            copy_run(0, 1);
+        }
+
         __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
             return lds_read<i32x4>(stage + xr + half[s] + i * WM * 16 * kStepBytes);
         }
@@ -504,18 +570,24 @@ struct Product {
             if constexpr (WTR) return read_tr<BN>(stage + kXBytes, wave % WN * NT + j, s);
             return lds_read<i32x4>(stage + wr + half[s] + j * 16 * kStepBytes);
         }
-        __device__ __forceinline__ float x_scale(uint32_t stage, int i) const {
-            return lds_read<float>(stage + kXBytes + kWBytes + ((wave / WN + i * WM) * 16 + (lane & 15)) * 4);
+        __device__ __forceinline__ float x_scale(uint32_t stage, int step, int i) const {
+            const int row = (wave / WN + i * WM) * 16 + (lane & 15);
+            return RUNS ? lds_read<float>(scales + step / kRun % 3 * kXsRun + row * 16 + step % kRun * 4)
+                        : lds_read<float>(stage + kXBytes + kWBytes + row * 4);
         }
         // the f-th read of half s: the weights' fragments (and scales), then the rows'
-        __device__ __forceinline__ void read(Frags &h, uint32_t stage, int f, int s) const {
+        __device__ __forceinline__ void read(Frags &h, uint32_t stage, int step, int f, int s) const {
             if constexpr (FORM == kMx4) {
-                const uint32_t at = stage + kXBytes + kWBytes + (lane & 15) * 8 + (lane >> 4) * 2 + s;
+                constexpr int kRow = RUNS ? 16 : 8;
                 const int i = f / 2;
+                const uint32_t own = (lane & 15) * kRow + (lane >> 4) * 2 + s;
+                const uint32_t xs = (RUNS ? scales + step / 2 % 3 * (kXsRun + kWsRun) + step % 2 * 8
+                                          : stage + kXBytes + kWBytes) + own;
+                const uint32_t ws = xs + (RUNS ? kXsRun : kXScale);
                 if (f % 2 == 0 && i < NT) h.w[i] = w(stage, i, s);
-                if (f % 2 == 1 && i < NT) h.ws[i] = lds_read<uint8_t>(at + kXScale + (wave % WN * NT + i) * 128);
+                if (f % 2 == 1 && i < NT) h.ws[i] = lds_read<uint8_t>(ws + (wave % WN * NT + i) * 16 * kRow);
                 if (f % 2 == 0 && i >= NT) h.x[i - NT] = x(stage, i - NT, s);
-                if (f % 2 == 1 && i >= NT) h.xs[i - NT] = lds_read<uint8_t>(at + (wave / WN + (i - NT) * WM) * 128);
+                if (f % 2 == 1 && i >= NT) h.xs[i - NT] = lds_read<uint8_t>(xs + (wave / WN + (i - NT) * WM) * 16 * kRow);
             } else {
                 if (f < NT)
                     h.w[f] = w(stage, f, s);
@@ -635,9 +707,9 @@ struct Product {
     }
 };
 
-template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
+template <int FORM, bool WTR, int BN, int WM, int WN, int MT, bool RUNS>
 __global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_product(ProductArgs a) {
-    using P = Product<FORM, WTR, BN, WM, WN, MT>;
+    using P = Product<FORM, WTR, BN, WM, WN, MT, RUNS>;
     __shared__ typename P::Shared sh;
     P::body(a, sh);
 }
@@ -668,7 +740,7 @@ struct Wgrad {
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
     using Frags = HalfFrags<ACT, NT, false>;
     static constexpr int kReads = ACT + NT;
-    static constexpr bool kAcc = ACT * NT >= 64;
+    static constexpr bool kAcc = ACT * NT >= 64, kRuns = false;
 
     struct Shared {
         uint8_t ring[kStages * kStage];
@@ -724,7 +796,8 @@ struct Wgrad {
     __device__ __forceinline__ i32x4 w(uint32_t stage, int j, int s) const {
         return read_tr<BN>(stage + kGBytes, wave % WN * NT + j, s);
     }
-    __device__ __forceinline__ void read(Frags &h, uint32_t stage, int f, int s) const {
+    __device__ __forceinline__ void first_run() const {}
+    __device__ __forceinline__ void read(Frags &h, uint32_t stage, int, int f, int s) const {
         if (f < NT)
             h.w[f] = w(stage, f, s);
         else
@@ -797,17 +870,25 @@ __global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_wgrad(WgradA
 // loop over the tiles), or fewer where there cannot be that many tiles.
 template <int FORM, bool WTR, int BN, int WM, int WN, int MT>
 hipError_t launch_product(const ProductArgs &a, int grid, hipStream_t s) {
-    k_product<FORM, WTR, BN, WM, WN, MT><<<grid, WM * WN * 64, 0, s>>>(a);
+    // the MXFP4 form's small tiles have too few rows for its waves to share a run out
+    constexpr bool kRuns = FORM == kFp8 || (FORM == kMx4 && BN >= 256);
+    if (kRuns && a.K % 512 == 0)
+        k_product<FORM, WTR, BN, WM, WN, MT, kRuns><<<grid, WM * WN * 64, 0, s>>>(a);
+    else
+        k_product<FORM, WTR, BN, WM, WN, MT, false><<<grid, WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
-// 256-channel tiles of up to 256 rows where there are enough of them for the
-// chip, else 128-channel tiles of up to 128 rows, two workgroups to a CU.
+// 256-channel tiles of up to 256 rows where the experts have rows for them and
+// there are enough for the chip, else 128-channel tiles of up to 128 rows, two
+// workgroups to a CU: where the weights' bytes are the time, one streams while
+// the other starts or ends its tile.
 template <int FORM, bool WTR>
 hipError_t launch_product_form(const ProductArgs &a, int64_t rows, int cus, hipStream_t s) {
     const int64_t experts = rows < a.g.E ? rows : a.g.E;
     const int64_t big = (rows / 256 > experts ? rows / 256 : experts) * ((a.N + 255) / 256);
-    if (big >= cus) return launch_product<FORM, WTR, 256, 2, FORM == kFp8 ? 4 : 2, 8>(a, cus, s);
+    if (rows > 64 * (int64_t)a.g.E && big >= cus)
+        return launch_product<FORM, WTR, 256, 2, FORM == kFp8 ? 4 : 2, 8>(a, cus, s);
     const int64_t most = (rows / 32 + experts) * ((a.N + 127) / 128);
     return launch_product<FORM, WTR, 128, 2, 2, 4>(a, (int)(most < 2 * cus ? most : 2 * cus), s);
 }
