@@ -65,6 +65,11 @@ __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
                  : "memory");
 }
+// the same for bytes that nothing reads again: they take no other line's place in the caches
+__device__ __forceinline__ void copy16_once(const uint8_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory");
+}
 __device__ __forceinline__ void copy4(const uint8_t *base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
                  : "memory");
@@ -405,8 +410,8 @@ struct Product {
         int tiles[3];
     };
 
-    // what a wave needs to copy and read a tile's steps, for ACT row tiles per wave
-    template <int ACT_>
+    // what a wave needs to copy and read a tile's steps, for ACT row tiles per wave; ONCE: no other tile reads these weights
+    template <int ACT_, bool ONCE>
     struct Tile {
         static constexpr int ACT = ACT_, NT = NTILES, ROWS = 16 * WM * ACT;
         static constexpr int kXBytes = ROWS * kStepBytes, kWBytes = BN * kStepBytes;
@@ -520,7 +525,9 @@ struct Product {
             } else if (c < kXPer + kWPer) {
                 const int i = c - kXPer, ins = (wave + i * kWaves) % kWIns;
                 const uint32_t to = stage + kXBytes + ins * 1024;
-                if (WHOLE) {
+                if (WHOLE && ONCE) {
+                    copy16_once(wb + step * wstep, wo[i], to);
+                } else if (WHOLE) {
                     copy16(wb + step * wstep, wo[i], to);
                 } else {
                     const bool ok = WTR ? step * 64 + (ins * 64 + lane) / (BN / 8) < K : in;
@@ -603,7 +610,7 @@ struct Product {
         }
     };
 
-    template <int ACT>
+    template <int ACT, bool ONCE>
     static __device__ __forceinline__ void tile(const ProductArgs &a, const Shared &sh, uint32_t ring, int wave,
                                                 int lane, int e, int n0, int rows) {
         const int wm = wave / WN, wn = wave % WN;
@@ -612,7 +619,7 @@ struct Product {
         for (int i = 0; i < ACT; ++i)
 #pragma unroll
             for (int j = 0; j < NTILES; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        const Tile<ACT> t(a, sh, wave, lane, e, n0);
+        const Tile<ACT, ONCE> t(a, sh, wave, lane, e, n0);
         if constexpr (FORM == kFp8) {
             static_assert(128 % (NTILES * 16) == 0, "a wave's channels share one weight scale");
             const int nb = min(n0 + wn * NTILES * 16, a.N - 1) / 128;
@@ -695,14 +702,22 @@ struct Product {
                 sh.row[i] = (int)ep::group_row(a.g, e, m0 + (i < rows ? i : rows - 1));
             __syncthreads();
             const int act = (rows + 16 * WM - 1) / (16 * WM);
+            // weights that only this tile reads are streamed past the caches (128 tokens' decode on 256 experts, 7.4 GB of
+            // weights: 1088 us against 1203); where several row tiles read them that loses (256 rows of one expert: 41
+            // against 29)
+            const bool once = BN < 256 && em == 1;
             if (MT >= 8 && act <= MT / 8)
-                tile<MT / 8 ? MT / 8 : 1>(a, sh, ring, wave, lane, e, n0, rows);
+                tile<MT / 8 ? MT / 8 : 1, false>(a, sh, ring, wave, lane, e, n0, rows);
+            else if (MT >= 4 && act <= MT / 4 && once)
+                tile<MT / 4 ? MT / 4 : 1, BN < 256>(a, sh, ring, wave, lane, e, n0, rows);
             else if (MT >= 4 && act <= MT / 4)
-                tile<MT / 4 ? MT / 4 : 1>(a, sh, ring, wave, lane, e, n0, rows);
+                tile<MT / 4 ? MT / 4 : 1, false>(a, sh, ring, wave, lane, e, n0, rows);
+            else if (MT >= 2 && act <= MT / 2 && once)
+                tile<MT / 2 ? MT / 2 : 1, BN < 256>(a, sh, ring, wave, lane, e, n0, rows);
             else if (MT >= 2 && act <= MT / 2)
-                tile<MT / 2 ? MT / 2 : 1>(a, sh, ring, wave, lane, e, n0, rows);
+                tile<MT / 2 ? MT / 2 : 1, false>(a, sh, ring, wave, lane, e, n0, rows);
             else
-                tile<MT>(a, sh, ring, wave, lane, e, n0, rows);
+                tile<MT, false>(a, sh, ring, wave, lane, e, n0, rows);
         }
     }
 };

@@ -2,9 +2,11 @@
 // SwiGLU and its gradient, MXFP4 quantization and back.
 //
 // All four read every value once and write every value once: they are bound
-// by memory. A wave takes chunks of a row (512 channels of SwiGLU, 8 a lane;
-// 2048 of MXFP4, 32 a lane, so that a lane holds whole scale groups), a run
-// of neighbouring chunks per wave, kUnroll chunks' loads in flight together.
+// by memory. A wave takes chunks of 512 channels of a row, 8 a lane (16 bytes
+// of bf16, neighbouring lanes neighbouring addresses: 32 channels a lane, a
+// whole scale group, took 2.3 times as long to write), a run of neighbouring
+// chunks per wave, kUnroll chunks' loads in flight together. A scale group of
+// 32 channels is four lanes, one of 128 sixteen.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -82,12 +84,14 @@ struct RowWalk {
 
 enum Op { kSwigluBf16, kSwigluFp8, kSwigluMx4, kSwigluGrad, kQuantize, kDequantize };
 
+constexpr int kPer = 8;     // channels per lane and chunk
+// chunks whose loads are in flight together: SwiGLU's gradient 260 us with 4, 267 with 2; MXFP4 there and back 155 and 129
 template <int OP>
-struct Lane {
-    static constexpr int kPer = OP == kSwigluMx4 || OP == kQuantize || OP == kDequantize ? 32 : 8;  // channels
-    static constexpr int kVecs = kPer / 8;
-    static constexpr int kUnroll = kPer == 8 ? 4 : 1;
-};
+constexpr int kUnroll = OP == kQuantize || OP == kDequantize ? 2 : 4;
+
+// 16-byte vectors that a lane loads
+template <int OP>
+constexpr int kVecs = OP == kSwigluGrad ? 3 : OP == kQuantize || OP == kDequantize ? 1 : 2;
 
 __device__ __forceinline__ u32x4 load16(const void *p) { return __builtin_nontemporal_load((const u32x4 *)p); }
 template <class T>
@@ -95,94 +99,71 @@ __device__ __forceinline__ void store(T v, void *p) {
     __builtin_nontemporal_store(v, (T *)p);
 }
 
-// the MXFP4 codes and scale byte of 32 values
-__device__ __forceinline__ u32x4 mx4_codes(const float (&f)[32], uint8_t &scale) {
+template <int CTRL>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float lane_max(float m) {
+    return fmaxf(m, __uint_as_float(from_lane<CTRL>(__float_as_uint(m))));
+}
+
+// Eight MXFP4 codes of a lane and the scale byte of its four lanes' group.
+__device__ __forceinline__ uint32_t mx4_codes(const float (&f)[8], uint8_t &scale) {
     uint32_t top = 0;  // the largest magnitude's bits: NaN and infinity keep the largest exponent
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    top = max(top, from_lane<0xB1>(top));
+    top = max(top, from_lane<0x4E>(top));
     const int field = (int)(top >> 23);        // floor(log2) + 127 of a normal number
     const bool bad = field == 255;
     const int e = max(field - 2, 0);           // the scale byte; subnormals and zeros: 0, which is 2^-127
     scale = bad ? 255 : (uint8_t)e;
     const float s = __uint_as_float(e == 0 ? 0x00400000u : (uint32_t)e << 23);
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t v = 0;
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[8 * i + 0], f[8 * i + 1], s, 0);
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[8 * i + 2], f[8 * i + 3], s, 1);
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[8 * i + 4], f[8 * i + 5], s, 2);
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[8 * i + 6], f[8 * i + 7], s, 3);
-        w[i] = bad ? 0 : v;
-    }
-    return w;
+    uint32_t v = 0;
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[0], f[1], s, 0);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[2], f[3], s, 1);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[4], f[5], s, 2);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, f[6], f[7], s, 3);
+    return bad ? 0 : v;
 }
 
 template <int OP>
 __device__ __forceinline__ void load_lane(const RowsArgs &a, int64_t row, int64_t c, u32x4 *v) {
-    constexpr int V = Lane<OP>::kVecs;
+    const int64_t at = row * a.cols + c;
     if constexpr (OP == kDequantize) {
-        v[0] = load16(a.q + (row * a.cols + c) / 2);
-        v[1].x = a.qs[(row * a.cols + c) / 32];
+        v[0].x = __builtin_nontemporal_load((const uint32_t *)(a.q + at / 2));
+        v[0].y = a.qs[at / 32];
     } else if constexpr (OP == kQuantize) {
-        const uint16_t *p = a.a + row * a.cols + c;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = load16(p + 8 * i);
+        v[0] = load16(a.a + at);
     } else {
         const uint16_t *p = a.a + row * 2 * a.cols + c;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = load16(p + 8 * i);
-            v[V + i] = load16(p + a.cols + 8 * i);
-        }
-        if constexpr (OP == kSwigluGrad) v[2 * V] = load16(a.d + row * a.cols + c);
+        v[0] = load16(p);
+        v[1] = load16(p + a.cols);
+        if constexpr (OP == kSwigluGrad) v[2] = load16(a.d + at);
     }
-}
-
-template <int CTRL>
-__device__ __forceinline__ float lane_max(float m) {
-    const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(m), CTRL, 0xF, 0xF, true);
-    return fmaxf(m, __int_as_float(o));
 }
 
 template <int OP>
 __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64_t c, const u32x4 *v) {
-    constexpr int V = Lane<OP>::kVecs;
     const int64_t at = row * a.cols + c;
     if constexpr (OP == kDequantize) {
         // scale byte b as fp32 2^(b-127); 255: NaN, which its product with any code is
-        const uint32_t b = v[1].x;
+        const uint32_t b = v[0].y;
         const float s = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+        u32x4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u32x4 o;
+        for (int k = 0; k < 4; ++k) {
+            float f[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t two = v[0][i] >> (8 * k);
-                float f[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // e2m1 as fp32: exponent and mantissa bits moved up, the bias (1 against 127) made up by 2^126
-                    const uint32_t code = two >> (4 * h);
-                    f[h] = __uint_as_float((code & 7) << 22 | (code & 8) << 28) * 0x1p126f * s;
-                }
-                o[k] = pack_bf16(f[0], f[1]);
+            for (int h = 0; h < 2; ++h) {
+                // e2m1 as fp32: exponent and mantissa bits moved up, the bias (1 against 127) made up by 2^126
+                const uint32_t code = v[0].x >> (8 * k + 4 * h);
+                f[h] = __uint_as_float((code & 7) << 22 | (code & 8) << 28) * 0x1p126f * s;
             }
-            store(o, (uint16_t *)a.out + at + 8 * i);
+            o[k] = pack_bf16(f[0], f[1]);
         }
-    } else if constexpr (OP == kQuantize) {
-        float f[32];
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f[8 * i + 2 * k] = lo16(v[i][k]);
-                f[8 * i + 2 * k + 1] = hi16(v[i][k]);
-            }
-        uint8_t s;
-        const u32x4 w = mx4_codes(f, s);
-        store(w, (uint8_t *)a.out + at / 2);
-        ((uint8_t *)a.scales)[at / 32] = s;
+        store(o, (uint16_t *)a.out + at);
     } else if constexpr (OP == kSwigluGrad) {
         u32x4 og, ou;
 #pragma unroll
@@ -203,27 +184,26 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
         store(og, o);
         store(ou, o + a.cols);
     } else {
-        float f[8 * V];
+        float f[8];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float g = h ? hi16(v[i][k]) : lo16(v[i][k]);
-                    const float u = h ? hi16(v[V + i][k]) : lo16(v[V + i][k]);
-                    f[8 * i + 2 * k + h] = g * sigmoid(g) * u;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const float g = h ? hi16(v[0][k]) : lo16(v[0][k]);
+                if constexpr (OP == kQuantize)
+                    f[2 * k + h] = g;
+                else
+                    f[2 * k + h] = g * sigmoid(g) * (h ? hi16(v[1][k]) : lo16(v[1][k]));
+            }
         if constexpr (OP == kSwigluBf16) {
             store(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])},
                   (uint16_t *)a.out + at);
-        } else if constexpr (OP == kSwigluMx4) {
+        } else if constexpr (OP == kSwigluMx4 || OP == kQuantize) {
             uint8_t s;
-            const u32x4 w = mx4_codes(f, s);
+            const uint32_t w = mx4_codes(f, s);
             store(w, (uint8_t *)a.out + at / 2);
-            ((uint8_t *)a.scales)[at / 32] = s;
+            if ((threadIdx.x & 3) == 0) ((uint8_t *)a.scales)[at / 32] = s;
         } else {
-            // a scale group is 16 lanes wide (128 channels); I % 128 == 0 keeps it within the active lanes
             float m = 0.0f, z = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -256,13 +236,13 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
 
 template <int OP>
 __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs a) {
-    constexpr int U = Lane<OP>::kUnroll, PER = Lane<OP>::kPer, VECS = OP == kDequantize ? 2 : 2 * Lane<OP>::kVecs + 1;
+    constexpr int U = kUnroll<OP>;
     __shared__ int ends[ep::kGroupsMaxExperts];
     const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
     const int lane = threadIdx.x & 63;
     const int64_t waves = (int64_t)gridDim.x * (kThreads / 64);
     const int64_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
-    const int64_t chunks = (a.cols + 64 * PER - 1) / (64 * PER);
+    const int64_t chunks = (a.cols + 64 * kPer - 1) / (64 * kPer);
     const int64_t items = rows * chunks, each = items / waves, more = items % waves;
     int64_t at = wave * each + (wave < more ? wave : more);
     const int64_t last = at + each + (wave < more ? 1 : 0);
@@ -271,13 +251,13 @@ __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs a) {
     RowWalk walk{&a.g, ends, 0, 0, 0, 0};
     int64_t row = a.grouped ? walk.row((int)entry) : entry;
     while (at < last) {
-        u32x4 v[U][VECS];
+        u32x4 v[U][kVecs<OP>];
         int64_t rows_u[U], cols_u[U];
         bool on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             rows_u[u] = row;
-            cols_u[u] = chunk * 64 * PER + lane * PER;
+            cols_u[u] = chunk * 64 * kPer + lane * kPer;
             on[u] = at < last && cols_u[u] < a.cols;
             if (on[u]) load_lane<OP>(a, row, cols_u[u], v[u]);
             if (++at < last && ++chunk == chunks) {
@@ -294,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs a) {
 
 template <int OP>
 hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
-    const int64_t chunks = (a.cols + 64 * Lane<OP>::kPer - 1) / (64 * Lane<OP>::kPer);
+    const int64_t chunks = (a.cols + 64 * kPer - 1) / (64 * kPer);
     const int64_t blocks = (rows * chunks + kThreads / 64 - 1) / (kThreads / 64);
     const int64_t most = (int64_t)cus * 8;
     k_rows<OP><<<(int)(blocks < 1 ? 1 : blocks < most ? blocks : most), kThreads, 0, s>>>(a);

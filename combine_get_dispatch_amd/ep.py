@@ -706,32 +706,50 @@ class Groups:
         return self.num_ranks * self.cap_rows
 
     def c(self) -> EpGroups:
-        import torch
+        return self._c(_device())
+
+    def _c(self, dev: int) -> EpGroups:
         shape = (self.num_experts, self.num_ranks) if self.region_rows else (self.num_experts,)
-        _tensor(self.counts, "counts", torch.int32, shape)
-        if self.offsets is not None:
-            _tensor(self.offsets, "offsets", torch.int32, shape)
-        return EpGroups(_ptr(self.offsets), self.counts.data_ptr(), self.num_experts, self.num_ranks, self.cap_rows,
-                        self.region_rows, self.rows_hint)
+        counts = _tensor(self.counts, "counts", _torch.int32, shape, dev)
+        offsets = None if self.offsets is None else _tensor(self.offsets, "offsets", _torch.int32, shape, dev)
+        return EpGroups(offsets, counts, self.num_experts, self.num_ranks, self.cap_rows, self.region_rows,
+                        self.rows_hint)
 
 
-def _tensor(t, what: str, dtype, shape) -> int:
-    """The pointer of a dense tensor of this type and shape on the current
-    device; anything else is refused (EP_ERR_ARG)."""
-    import torch
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+_torch = None
+
+
+def _device() -> int:
+    """The current GPU's index (-1 without one: every tensor is refused then)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if _torch.cuda.is_initialized():
+        return _torch._C._cuda_getDevice()
+    return _torch.cuda.current_device() if _torch.cuda.is_available() else -1
+
+
+def _tensor(t, what: str, dtype, shape, dev: int) -> int:
+    """The pointer of a dense tensor of this type and shape on GPU ``dev``, the
+    current one; anything else is refused (EP_ERR_ARG)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
         raise EpError(EP_ERR_ARG, f"{what}: {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
     if not t.is_contiguous():
         raise EpError(EP_ERR_ARG, f"{what} is not contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise EpError(EP_ERR_ARG, f"{what} is on {t.device}, not on the current GPU")
-    return t.data_ptr()
+    raise EpError(EP_ERR_ARG, f"{what} is on {t.device}, not on the current GPU")
 
 
 def _shape(t, what: str, dims: int):
     if t.dim() != dims:
         raise EpError(EP_ERR_ARG, f"{what}: {t.dim()} dimensions, not {dims}")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _raw_stream(dev: int) -> int:
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def expert_gemm(rows, weights, groups: Groups, row_scales=None, weight_scales=None, out=None):
@@ -747,42 +765,43 @@ def expert_gemm(rows, weights, groups: Groups, row_scales=None, weight_scales=No
              row_scales [R*cap_rows, K/32], weight_scales [E, N, K/32]
              (quantize_mxfp4 writes both)
     """
-    import torch
-    g = groups.c()
+    dev = _device()
+    g = groups._c(dev)
     E, N, width = _shape(weights, "weights", 3)
     n = groups.num_rows
     if (row_scales is None) != (weight_scales is None):
         raise EpError(EP_ERR_ARG, "rows and weights need scales both, or neither")
     if row_scales is None:
-        form, K, dtype, rs, ws = EP_FORM_BF16, width, torch.bfloat16, None, None
-    elif row_scales.dtype == torch.float32:
-        form, K, dtype = EP_FORM_FP8, width, torch.uint8
-        rs = _tensor(row_scales, "row_scales", torch.float32, (n, K // 128))
-        ws = _tensor(weight_scales, "weight_scales", torch.float32, (groups.num_experts, (N + 127) // 128, K // 128))
+        form, K, dtype, rs, ws = EP_FORM_BF16, width, _torch.bfloat16, None, None
+    elif row_scales.dtype == _torch.float32:
+        form, K, dtype = EP_FORM_FP8, width, _torch.uint8
+        rs = _tensor(row_scales, "row_scales", _torch.float32, (n, K // 128), dev)
+        ws = _tensor(weight_scales, "weight_scales", _torch.float32,
+                     (groups.num_experts, (N + 127) // 128, K // 128), dev)
     else:
-        form, K, dtype = EP_FORM_MXFP4, 2 * width, torch.uint8
-        rs = _tensor(row_scales, "row_scales", torch.uint8, (n, K // 32))
-        ws = _tensor(weight_scales, "weight_scales", torch.uint8, (groups.num_experts, N, K // 32))
-    x = _tensor(rows, "rows", dtype, (n, width))
-    w = _tensor(weights, "weights", dtype, (groups.num_experts, N, width))
+        form, K, dtype = EP_FORM_MXFP4, 2 * width, _torch.uint8
+        rs = _tensor(row_scales, "row_scales", _torch.uint8, (n, K // 32), dev)
+        ws = _tensor(weight_scales, "weight_scales", _torch.uint8, (groups.num_experts, N, K // 32), dev)
+    x = _tensor(rows, "rows", dtype, (n, width), dev)
+    w = _tensor(weights, "weights", dtype, (groups.num_experts, N, width), dev)
     if out is None:
-        out = torch.empty((n, N), dtype=torch.bfloat16, device=rows.device)
-    ep_expert_gemm(g, form, x, rs, w, ws, K, N, _tensor(out, "out", torch.bfloat16, (n, N)), _stream())
+        out = _torch.empty((n, N), dtype=_torch.bfloat16, device=rows.device)
+    ep_expert_gemm(g, form, x, rs, w, ws, K, N, _tensor(out, "out", _torch.bfloat16, (n, N), dev), _raw_stream(dev))
     return out
 
 
 def expert_gemm_dgrad(grad_out, weights, groups: Groups, out=None):
     """Gradient of the bf16 ``expert_gemm`` in its rows: grad_out [R*cap_rows,
     N], weights [E, N, K] -> [R*cap_rows, K], all bfloat16."""
-    import torch
-    g = groups.c()
+    dev = _device()
+    g = groups._c(dev)
     E, N, K = _shape(weights, "weights", 3)
     n = groups.num_rows
-    d = _tensor(grad_out, "grad_out", torch.bfloat16, (n, N))
-    w = _tensor(weights, "weights", torch.bfloat16, (groups.num_experts, N, K))
+    d = _tensor(grad_out, "grad_out", _torch.bfloat16, (n, N), dev)
+    w = _tensor(weights, "weights", _torch.bfloat16, (groups.num_experts, N, K), dev)
     if out is None:
-        out = torch.empty((n, K), dtype=torch.bfloat16, device=weights.device)
-    ep_expert_gemm_dgrad(g, d, w, K, N, _tensor(out, "out", torch.bfloat16, (n, K)), _stream())
+        out = _torch.empty((n, K), dtype=_torch.bfloat16, device=weights.device)
+    ep_expert_gemm_dgrad(g, d, w, K, N, _tensor(out, "out", _torch.bfloat16, (n, K), dev), _raw_stream(dev))
     return out
 
 
@@ -791,23 +810,24 @@ def expert_gemm_wgrad(grad_out, rows, groups: Groups, out=None, dtype=None, accu
     [R*cap_rows, N], rows [R*cap_rows, K] bfloat16 -> [E, N, K] of ``dtype``
     (float32, the default, or bfloat16; ``out``'s own where it is given).
     ``accumulate`` adds to a float32 ``out``."""
-    import torch
-    g = groups.c()
+    dev = _device()
+    g = groups._c(dev)
     n, N = _shape(grad_out, "grad_out", 2)
     _, K = _shape(rows, "rows", 2)
     if accumulate and out is None:
         raise EpError(EP_ERR_ARG, "accumulate needs the out to add to")
     if out is not None and dtype is not None and out.dtype != dtype:
         raise EpError(EP_ERR_ARG, f"out is {out.dtype}, not {dtype}")
-    dtype = out.dtype if out is not None else dtype or torch.float32
-    if dtype not in (torch.float32, torch.bfloat16):
+    dtype = out.dtype if out is not None else dtype or _torch.float32
+    if dtype not in (_torch.float32, _torch.bfloat16):
         raise EpError(EP_ERR_ARG, f"weight gradients are float32 or bfloat16, not {dtype}")
-    d = _tensor(grad_out, "grad_out", torch.bfloat16, (groups.num_rows, N))
-    x = _tensor(rows, "rows", torch.bfloat16, (groups.num_rows, K))
+    d = _tensor(grad_out, "grad_out", _torch.bfloat16, (groups.num_rows, N), dev)
+    x = _tensor(rows, "rows", _torch.bfloat16, (groups.num_rows, K), dev)
     shape = (groups.num_experts, N, K)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=rows.device)
-    ep_expert_gemm_wgrad(g, d, x, K, N, _tensor(out, "out", dtype, shape), dtype == torch.float32, accumulate, _stream())
+        out = _torch.empty(shape, dtype=dtype, device=rows.device)
+    ep_expert_gemm_wgrad(g, d, x, K, N, _tensor(out, "out", dtype, shape, dev), dtype == _torch.float32, accumulate,
+                         _raw_stream(dev))
     return out
 
 
@@ -818,38 +838,38 @@ def swiglu(gate_up, groups: Optional[Groups] = None, kind: str = "bf16", out=Non
     "mxfp4" (uint8 [num_rows, I/2], uint8 scales [num_rows, I/32]) return what
     the next ``expert_gemm`` reads; ``out`` is of the same form. With
     ``groups`` only the rows experts have are computed and written."""
-    import torch
+    dev = _device()
     n, I = _shape(gate_up, "gate_up", 2)
     I //= 2
-    x = _tensor(gate_up, "gate_up", torch.bfloat16, (n, 2 * I))
+    x = _tensor(gate_up, "gate_up", _torch.bfloat16, (n, 2 * I), dev)
     if kind == "bf16":
-        form, spec = EP_FORM_BF16, (((n, I), torch.bfloat16),)
+        form, spec = EP_FORM_BF16, (((n, I), _torch.bfloat16),)
     elif kind == "fp8":
-        form, spec = EP_FORM_FP8, (((n, I), torch.uint8), ((n, I // 128), torch.float32))
+        form, spec = EP_FORM_FP8, (((n, I), _torch.uint8), ((n, I // 128), _torch.float32))
     elif kind == "mxfp4":
-        form, spec = EP_FORM_MXFP4, (((n, I // 2), torch.uint8), ((n, I // 32), torch.uint8))
+        form, spec = EP_FORM_MXFP4, (((n, I // 2), _torch.uint8), ((n, I // 32), _torch.uint8))
     else:
         raise EpError(EP_ERR_ARG, f"kind {kind!r} is none of bf16, fp8, mxfp4")
     outs = (out,) if kind == "bf16" and out is not None else out
     if outs is None:
-        outs = tuple(torch.empty(s, dtype=t, device=gate_up.device) for s, t in spec)
-    ptrs = [_tensor(o, w, t, s) for o, w, (s, t) in zip(outs, ("out", "scales"), spec)]
-    ep_swiglu(None if groups is None else groups.c(), x, n, I, form, ptrs[0], ptrs[1] if len(ptrs) > 1 else None,
-              _stream())
+        outs = tuple(_torch.empty(s, dtype=t, device=gate_up.device) for s, t in spec)
+    ptrs = [_tensor(o, w, t, s, dev) for o, w, (s, t) in zip(outs, ("out", "scales"), spec)]
+    ep_swiglu(None if groups is None else groups._c(dev), x, n, I, form, ptrs[0], ptrs[1] if len(ptrs) > 1 else None,
+              _raw_stream(dev))
     return outs[0] if kind == "bf16" else tuple(outs)
 
 
 def swiglu_backward(grad_out, gate_up, groups: Optional[Groups] = None, out=None):
     """Gradient of ``swiglu`` in gate_up [num_rows, 2*I]: grad_out [num_rows,
     I] -> [num_rows, 2*I], all bfloat16. ``out`` may be ``gate_up``."""
-    import torch
+    dev = _device()
     n, I = _shape(grad_out, "grad_out", 2)
-    d = _tensor(grad_out, "grad_out", torch.bfloat16, (n, I))
-    x = _tensor(gate_up, "gate_up", torch.bfloat16, (n, 2 * I))
+    d = _tensor(grad_out, "grad_out", _torch.bfloat16, (n, I), dev)
+    x = _tensor(gate_up, "gate_up", _torch.bfloat16, (n, 2 * I), dev)
     if out is None:
-        out = torch.empty((n, 2 * I), dtype=torch.bfloat16, device=gate_up.device)
-    ep_swiglu_backward(None if groups is None else groups.c(), d, x, n, I,
-                       _tensor(out, "out", torch.bfloat16, (n, 2 * I)), _stream())
+        out = _torch.empty((n, 2 * I), dtype=_torch.bfloat16, device=gate_up.device)
+    ep_swiglu_backward(None if groups is None else groups._c(dev), d, x, n, I,
+                       _tensor(out, "out", _torch.bfloat16, (n, 2 * I), dev), _raw_stream(dev))
     return out
 
 
@@ -857,31 +877,31 @@ def quantize_mxfp4(x, groups: Optional[Groups] = None, out=None):
     """MXFP4 form of the bfloat16 rows of x [..., cols] (weights [E, N, K] as
     well as rows): (uint8 [..., cols/2], uint8 scales [..., cols/32]). With
     ``groups`` (x [R*cap_rows, cols]) only the rows experts have."""
-    import torch
+    dev = _device()
     cols = x.shape[-1] if x.dim() else 0
     n = x.numel() // cols if cols else 0
-    p = _tensor(x, "x", torch.bfloat16, x.shape)
+    p = _tensor(x, "x", _torch.bfloat16, x.shape, dev)
     shapes = tuple(x.shape[:-1]) + (cols // 2,), tuple(x.shape[:-1]) + (cols // 32,)
     if out is None:
-        out = tuple(torch.empty(s, dtype=torch.uint8, device=x.device) for s in shapes)
+        out = tuple(_torch.empty(s, dtype=_torch.uint8, device=x.device) for s in shapes)
     q, scales = out
-    ep_quantize_mxfp4(None if groups is None else groups.c(), p, n, cols, _tensor(q, "q", torch.uint8, shapes[0]),
-                      _tensor(scales, "scales", torch.uint8, shapes[1]), _stream())
+    ep_quantize_mxfp4(None if groups is None else groups._c(dev), p, n, cols,
+                      _tensor(q, "q", _torch.uint8, shapes[0], dev), _tensor(scales, "scales", _torch.uint8, shapes[1], dev), _raw_stream(dev))
     return q, scales
 
 
 def dequantize_mxfp4(q, scales, groups: Optional[Groups] = None, out=None):
     """The bfloat16 values [..., cols] that quantize_mxfp4's (q, scales) stand for."""
-    import torch
+    dev = _device()
     cols = 2 * q.shape[-1] if q.dim() else 0
     n = 2 * q.numel() // cols if cols else 0
     shape = tuple(q.shape[:-1]) + (cols,)
-    p = _tensor(q, "q", torch.uint8, q.shape)
-    s = _tensor(scales, "scales", torch.uint8, tuple(q.shape[:-1]) + (cols // 32,))
+    p = _tensor(q, "q", _torch.uint8, q.shape, dev)
+    s = _tensor(scales, "scales", _torch.uint8, tuple(q.shape[:-1]) + (cols // 32,), dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    ep_dequantize_mxfp4(None if groups is None else groups.c(), p, s, n, cols,
-                        _tensor(out, "out", torch.bfloat16, shape), _stream())
+        out = _torch.empty(shape, dtype=_torch.bfloat16, device=q.device)
+    ep_dequantize_mxfp4(None if groups is None else groups._c(dev), p, s, n, cols,
+                        _tensor(out, "out", _torch.bfloat16, shape, dev), _raw_stream(dev))
     return out
 
 
