@@ -55,6 +55,13 @@ struct ProductArgs {
 // copies to LDS and waits
 // ---------------------------------------------------------------------------
 
+// a pointer that is the same in every lane, in scalar registers as the copies' base has to be
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t *)((uint64_t)hi << 32 | lo);
+}
+
 // Copy 16 (4) bytes per lane from base + off to LDS at `lds` + 16 (4) * lane;
 // base and lds are the same in every lane. Written as asm because the
 // compiler, which cannot tell the ring's buffers apart, otherwise waits for
@@ -62,24 +69,27 @@ struct ProductArgs {
 // register, and the waits are wait_copies() below. M0 holds the LDS address
 // and needs one wait state before its use.
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+    base = uniform(base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 // the same for bytes that nothing reads again: they take no other line's place in the caches
 __device__ __forceinline__ void copy16_once(const uint8_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(lds)
+    base = uniform(base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
+    base = uniform(base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 // the same with an address per lane
 __device__ __forceinline__ void copy16(const uint8_t *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 
 // Wait until at most `N` of this wave's copies are in flight and its LDS
@@ -94,13 +104,6 @@ __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
-}
-
-// a pointer that is the same in every lane, as the copies' base has to be
-__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const uint8_t *)((uint64_t)hi << 32 | lo);
 }
 
 template <class T>
@@ -203,23 +206,39 @@ __device__ __forceinline__ void settle() {
 // the reduction
 // ---------------------------------------------------------------------------
 
-// The ring's first steps: whole ones, then those with chunks past the end.
+// Copies first..last of a step into its buffer: a whole step's, or one's with
+// chunks past the end.
 template <class P>
-__device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, int whole) {
-    if (P::kRuns) p.first_run();
+__device__ __forceinline__ void copy_step(const P &p, uint32_t stage, int step, int whole, int first, int last) {
+    if (step < whole) {
 #pragma unroll
-    for (int i = 0; i < P::kStages; ++i) {
-        if (i < whole) {
+        for (int c = 0; c < P::kPer; ++c)
+            if (c >= first && c < last) p.template copy<true>(step, stage, c);
+    } else if (!P::kRuns) {  // with runs of scales all steps are whole
 #pragma unroll
-            for (int c = 0; c < P::kPer; ++c) p.template copy<true>(i, ring + i * P::kStage, c);
-        } else if (i < steps) {
-#pragma unroll
-            for (int c = 0; c < P::kPer; ++c) p.template copy<false>(i, ring + i * P::kStage, c);
-        }
+        for (int c = 0; c < P::kPer; ++c)
+            if (c >= first && c < last) p.template copy<false>(step, stage, c);
     }
 }
 
-enum Copies { kNone, kWhole, kPartial };
+// The ring's first steps, of the last buffer's only the copies that a step's
+// predecessors make (kSoon), and the wait for the first.
+template <class P>
+__device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, int whole) {
+    constexpr int S = P::kStages;
+    if (P::kRuns) p.first_run();
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < steps) copy_step(p, ring + i * P::kStage, i, whole, 0, i == S - 1 ? P::kSoon : P::kPer);
+    if (S <= steps)
+        wait_copies<(S - 2) * P::kPer + P::kSoon>();
+    else
+        wait_copies<0>();
+}
+
+// What a step copies: the step before it left the later copies of the ring's last buffer (kLate) to it, and the
+// first copies of the buffer it reads out itself (kSoon) follow; kLast: only the former, if there are any.
+enum Copies { kLast, kWhole, kPartial };
 
 // One tile's reduction for a wave: acc[i][j] += the products of the rows'
 // side fragment i < ACT and the weights' side fragment j < NT over all steps,
@@ -236,49 +255,49 @@ template <class P>
 __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
     constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
     fill_ring(p, ring, steps, whole);
-    if (S <= steps)
-        wait_copies<(S - 1) * P::kPer>();
-    else
-        wait_copies<0>();
     typename P::Frags h0, h1;
 #pragma unroll
     for (int f = 0; f < P::kReads; ++f) p.read(h0, ring, 0, f, 0);
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
-        constexpr int M = ACT * NT, I1 = P::kReads, I2 = P::kReads + (COPIES != kNone ? P::kPer : 0);
+        constexpr int M = ACT * NT, R = P::kReads, SOON = P::kSoon, LATE = P::kPer - SOON, L = M >= 4 ? M / 4 : M;
+        const uint32_t pv = ring + (slot == 0 ? S - 1 : slot - 1) * P::kStage;
         const uint32_t st = ring + slot * P::kStage;
         slot = slot + 1 == S ? 0 : slot + 1;
         const uint32_t nx = ring + slot * P::kStage;
+        if (COPIES == kLast) p.hold_scales(h0);
+        if (COPIES == kPartial || (COPIES == kLast && step + S - 1 < steps))
+            copy_step(p, pv, step + S - 1, whole, SOON, P::kPer);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
 #pragma unroll
-            for (int f = m * I1 / M; f < (m + 1) * I1 / M; ++f) p.read(h1, st, step, f, 1);
+            for (int f = m * LATE / L; f < (m + 1) * LATE / L && f < LATE; ++f)
+                if (COPIES == kWhole) p.template copy<true>(step + S - 1, pv, SOON + f);
+#pragma unroll
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h1, st, step, f, 1);
             p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
-        wait_copies<(COPIES == kNone ? 0 : (S - 2) * P::kPer)>();
+        wait_copies<(COPIES == kLast ? 0 : (S - 2) * P::kPer)>();
+        if (COPIES == kPartial) copy_step(p, st, step + S, whole, 0, SOON);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
 #pragma unroll
-            for (int f = m * I2 / M; f < (m + 1) * I2 / M; ++f) {
-                // reads and copies in turn
-                const int c = f * P::kPer / I2;
-                if (COPIES != kNone && (f + 1) * P::kPer / I2 > c)
-                    p.template copy<COPIES == kWhole>(step + S, st, c);
-                else
-                    p.read(h0, nx, step + 1, COPIES != kNone ? f - c : f, 0);
-            }
+            for (int f = m * SOON / M; f < (m + 1) * SOON / M; ++f)
+                if (COPIES == kWhole) p.template copy<true>(step + S, st, f);
+#pragma unroll
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h0, nx, step + 1, f, 0);
             p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
-        if (P::kAcc && COPIES == kNone) settle();
+        if (P::kAcc && COPIES == kLast) settle();
         ++step;
     };
     while (step + S < whole) body(std::integral_constant<int, kWhole>());
-    if (!P::kRuns)  // with runs of scales all steps are whole
+    if (!P::kRuns)
         while (step + S < steps) body(std::integral_constant<int, kPartial>());
-    while (step < steps) body(std::integral_constant<int, kNone>());
+    while (step < steps) body(std::integral_constant<int, kLast>());
 }
 
 // The FP8 form's reduction: a step is one block of 128 channels, its products
@@ -293,10 +312,6 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
     constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
     static_assert(ACT == 1 || ACT % 2 == 0, "row tiles alternate between two registers");
     fill_ring(p, ring, steps, steps);
-    if (S <= steps)
-        wait_copies<(S - 1) * P::kPer>();
-    else
-        wait_copies<0>();
     i32x8 w[NT], x[2];
     f32x4 part[2][NT];
 #pragma unroll
@@ -310,15 +325,18 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
+        const uint32_t pv = ring + (slot == 0 ? S - 1 : slot - 1) * P::kStage;
         const uint32_t st = ring + slot * P::kStage;
         slot = slot + 1 == S ? 0 : slot + 1;
         const uint32_t nx = ring + slot * P::kStage;
+        constexpr int SOON = P::kSoon, LATE = P::kPer - SOON, L = ACT * NT >= 8 ? ACT * NT * 3 / 8 : ACT * NT;
+        if (COPIES == kLast && step + S - 1 < steps) copy_step(p, pv, step + S - 1, steps, SOON, P::kPer);
         const float ws_next = w_scales[step + 1 < steps ? step + 1 : step];
 #pragma unroll
         for (int i = 0; i < ACT; ++i) {
             const bool last = i == ACT - 1;
             if (last) {  // the step's buffer has been read out, the next one's must have landed
-                wait_copies<(COPIES == kNone ? 0 : (S - 2) * P::kPer)>();
+                wait_copies<(COPIES == kLast ? 0 : (S - 2) * P::kPer)>();
             }
             f_prev = f;
             f = s_next * ws;
@@ -333,13 +351,15 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
             for (int j = 0; j < NT; ++j) {
                 const f32x4 before = part[(i + 1) & 1][j];
                 part[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    w[j], x[i & 1], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-                if (last) {
-                    if (COPIES != kNone) {
+                    w[j], x[i & 1], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                const int m = i * NT + j;
 #pragma unroll
-                        for (int c = j * P::kPer / NT; c < (j + 1) * P::kPer / NT; ++c)
-                            p.template copy<true>(step + S, st, c);
-                    }
+                for (int c = m * LATE / L; c < (m + 1) * LATE / L && c < LATE; ++c)
+                    if (COPIES == kWhole) p.template copy<true>(step + S - 1, pv, SOON + c);
+                if (last) {
+#pragma unroll
+                    for (int c = j * SOON / NT; c < (j + 1) * SOON / NT; ++c)
+                        if (COPIES == kWhole) p.template copy<true>(step + S, st, c);
                     w[j] = join(p.w(nx, j, 0), p.w(nx, j, 1));
                 }
                 const int to = (i + ACT - 1) % ACT;
@@ -358,7 +378,7 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
         ++step;
     };
     while (step + S < steps) body(std::integral_constant<int, kWhole>());
-    while (step < steps) body(std::integral_constant<int, kNone>());
+    while (step < steps) body(std::integral_constant<int, kLast>());
     if (ACT > 1) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -428,6 +448,8 @@ struct Product {
         static constexpr int kXsIns = kXScale / 256, kWsIns = kWScale / 256;
         static constexpr int kXsPer = (kXsIns + kWaves - 1) / kWaves, kWsPer = (kWsIns + kWaves - 1) / kWaves;
         static constexpr int kPer = kXPer + kWPer + (RUNS ? 1 : kXsPer + kWsPer);
+        // of these, made right when a buffer is free; the others in the step after
+        static constexpr int kSoon = FORM == kFp8 ? (ACT == 1 ? kPer : kPer / 3) : kPer * 4 / 5;
         static_assert(kStages >= 2 && kPer * (kStages - 1) < 64, "ring");
         using Frags = HalfFrags<ACT, NT, FORM == kMx4>;
         static constexpr int kReads = (FORM == kMx4 ? 2 : 1) * (ACT + NT);
@@ -602,6 +624,16 @@ struct Product {
                     h.x[f - NT] = x(stage, f - NT, s);
             }
         }
+        // Before a branch: the compiler would widen the scale bytes again behind it, right before the asm that reads them.
+        __device__ __forceinline__ void hold_scales(Frags &h) const {
+            if constexpr (FORM == kMx4 && kAcc) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(h.ws[j]));
+#pragma unroll
+                for (int i = 0; i < ACT; ++i) asm volatile("" : "+v"(h.xs[i]));
+                asm volatile("s_nop 1");
+            }
+        }
         __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
             if constexpr (FORM == kMx4)
                 mfma_mx4<kAcc>(h.w[j], h.x[i], c, h.ws[j], h.xs[i]);
@@ -752,6 +784,7 @@ struct Wgrad {
     static constexpr int ACT = BM / 16 / WM, NT = BN / 16 / WN;
     static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes, kStages = 2;
     static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + kXPer;
+    static constexpr int kSoon = kPer * 4 / 5;
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
     using Frags = HalfFrags<ACT, NT, false>;
     static constexpr int kReads = ACT + NT;
@@ -818,6 +851,7 @@ struct Wgrad {
         else
             h.x[f - NT] = x(stage, f - NT, s);
     }
+    __device__ __forceinline__ void hold_scales(Frags &) const {}
     __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
         mfma_bf16<kAcc>(h.w[j], h.x[i], c);
     }
