@@ -236,8 +236,7 @@ __device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, 
         wait_copies<0>();
 }
 
-// What a step copies: the step before it left the later copies of the ring's last buffer (kLate) to it, and the
-// first copies of the buffer it reads out itself (kSoon) follow; kLast: only the former, if there are any.
+// What a step copies into the buffer that it reads out: a whole step, one with chunks past the rows' end, nothing more.
 enum Copies { kLast, kWhole, kPartial };
 
 // One tile's reduction for a wave: acc[i][j] += the products of the rows'
@@ -261,31 +260,23 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
-        constexpr int M = ACT * NT, R = P::kReads, SOON = P::kSoon, LATE = P::kPer - SOON, L = M >= 4 ? M / 4 : M;
-        const uint32_t pv = ring + (slot == 0 ? S - 1 : slot - 1) * P::kStage;
+        constexpr int M = ACT * NT, R = P::kReads, C = P::kPer;
         const uint32_t st = ring + slot * P::kStage;
         slot = slot + 1 == S ? 0 : slot + 1;
         const uint32_t nx = ring + slot * P::kStage;
-        if (COPIES == kLast) p.hold_scales(h0);
-        if (COPIES == kPartial || (COPIES == kLast && step + S - 1 < steps))
-            copy_step(p, pv, step + S - 1, whole, SOON, P::kPer);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-#pragma unroll
-            for (int f = m * LATE / L; f < (m + 1) * LATE / L && f < LATE; ++f)
-                if (COPIES == kWhole) p.template copy<true>(step + S - 1, pv, SOON + f);
 #pragma unroll
             for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h1, st, step, f, 1);
             p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
         wait_copies<(COPIES == kLast ? 0 : (S - 2) * P::kPer)>();
-        if (COPIES == kPartial) copy_step(p, st, step + S, whole, 0, SOON);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
 #pragma unroll
-            for (int f = m * SOON / M; f < (m + 1) * SOON / M; ++f)
-                if (COPIES == kWhole) p.template copy<true>(step + S, st, f);
+            for (int f = m * C / M; f < (m + 1) * C / M; ++f)
+                if (COPIES != kLast) p.template copy<COPIES == kWhole>(step + S, st, f);
 #pragma unroll
             for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h0, nx, step + 1, f, 0);
             p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
@@ -449,7 +440,7 @@ struct Product {
         static constexpr int kXsPer = (kXsIns + kWaves - 1) / kWaves, kWsPer = (kWsIns + kWaves - 1) / kWaves;
         static constexpr int kPer = kXPer + kWPer + (RUNS ? 1 : kXsPer + kWsPer);
         // of these, made right when a buffer is free; the others in the step after
-        static constexpr int kSoon = FORM == kFp8 ? (ACT == 1 ? kPer : kPer / 3) : kPer * 4 / 5;
+        static constexpr int kSoon = FORM == kFp8 && ACT > 1 ? kPer / 3 : kPer;
         static_assert(kStages >= 2 && kPer * (kStages - 1) < 64, "ring");
         using Frags = HalfFrags<ACT, NT, FORM == kMx4>;
         static constexpr int kReads = (FORM == kMx4 ? 2 : 1) * (ACT + NT);
@@ -624,16 +615,6 @@ struct Product {
                     h.x[f - NT] = x(stage, f - NT, s);
             }
         }
-        // Before a branch: the compiler would widen the scale bytes again behind it, right before the asm that reads them.
-        __device__ __forceinline__ void hold_scales(Frags &h) const {
-            if constexpr (FORM == kMx4 && kAcc) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(h.ws[j]));
-#pragma unroll
-                for (int i = 0; i < ACT; ++i) asm volatile("" : "+v"(h.xs[i]));
-                asm volatile("s_nop 1");
-            }
-        }
         __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
             if constexpr (FORM == kMx4)
                 mfma_mx4<kAcc>(h.w[j], h.x[i], c, h.ws[j], h.xs[i]);
@@ -784,7 +765,7 @@ struct Wgrad {
     static constexpr int ACT = BM / 16 / WM, NT = BN / 16 / WN;
     static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes, kStages = 2;
     static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + kXPer;
-    static constexpr int kSoon = kPer * 4 / 5;
+    static constexpr int kSoon = kPer;
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
     using Frags = HalfFrags<ACT, NT, false>;
     static constexpr int kReads = ACT + NT;
@@ -851,7 +832,6 @@ struct Wgrad {
         else
             h.x[f - NT] = x(stage, f - NT, s);
     }
-    __device__ __forceinline__ void hold_scales(Frags &) const {}
     __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
         mfma_bf16<kAcc>(h.w[j], h.x[i], c);
     }
