@@ -28,7 +28,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // read through the scalar cache: the kernels never write it
 typedef const __attribute__((address_space(4))) float *constant_f32;
@@ -115,6 +116,33 @@ __device__ __forceinline__ uint16_t bf16_of(float f) {
     // round to nearest even; the hardware's conversion keeps NaN a NaN
     const __bf16 b = (__bf16)f;
     return __builtin_bit_cast(uint16_t, b);
+}
+
+// A row of 16 x 16 results as bf16: `c` four neighbouring 16-channel tiles of
+// a lane (row l & 15, channels 4 (l >> 4) + [0, 4) of each). Lanes exchange
+// them, 4 x 4 among the groups of 16, so that a lane holds its row's 16
+// channels of tile l >> 4: 32 bytes, 128 of a row with its neighbours' (four
+// times fewer memory lines a store than straight from the accumulators).
+__device__ __forceinline__ void to_row(const f32x4 *c, u32x4 (&out)[2]) {
+    uint32_t d[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        d[j][0] = bf16_of(c[j].x) | (uint32_t)bf16_of(c[j].y) << 16;
+        d[j][1] = bf16_of(c[j].z) | (uint32_t)bf16_of(c[j].w) << 16;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        u32x2 s;
+        // halves of the wave between tiles 0, 2 and 1, 3, then neighbouring groups between 0, 1 and 2, 3
+#define EP_SWAP(fn, i, j) s = fn(d[i][k], d[j][k], false, false), d[i][k] = s.x, d[j][k] = s.y
+        EP_SWAP(__builtin_amdgcn_permlane32_swap, 0, 2);
+        EP_SWAP(__builtin_amdgcn_permlane32_swap, 1, 3);
+        EP_SWAP(__builtin_amdgcn_permlane16_swap, 0, 1);
+        EP_SWAP(__builtin_amdgcn_permlane16_swap, 2, 3);
+#undef EP_SWAP
+    }
+    out[0] = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
+    out[1] = u32x4{d[2][0], d[2][1], d[3][0], d[3][1]};
 }
 
 // ---------------------------------------------------------------------------
@@ -644,14 +672,14 @@ struct Product {
 #pragma unroll
         for (int i = 0; i < ACT; ++i) {
             const int m = (wm + i * WM) * 16 + (lane & 15);
-            if (m >= rows) continue;
-            uint16_t *o = a.out + (int64_t)sh.row[m] * a.N;
+            uint16_t *o = a.out + (int64_t)sh.row[m < rows ? m : 0] * a.N;
 #pragma unroll
-            for (int j = 0; j < NTILES; ++j) {
-                const int n = n0 + (wn * NTILES + j) * 16 + (lane >> 4) * 4;
-                if (n < a.N)
-                    *(u16x4 *)(o + n) =
-                        u16x4{bf16_of(acc[i][j].x), bf16_of(acc[i][j].y), bf16_of(acc[i][j].z), bf16_of(acc[i][j].w)};
+            for (int j = 0; j < NTILES; j += 4) {
+                u32x4 v[2];
+                to_row(acc[i] + j, v);
+                const int n = n0 + (wn * NTILES + j + (lane >> 4)) * 16;
+                if (m < rows && n < a.N) *(u32x4 *)(o + n) = v[0];
+                if (m < rows && n + 8 < a.N) *(u32x4 *)(o + n + 8) = v[1];
             }
         }
     }
@@ -865,18 +893,23 @@ struct Wgrad {
 #pragma unroll
             for (int i = 0; i < ACT; ++i) {
                 const int n = n0 + (wm + i * WM) * 16 + (lane & 15);
-                if (n >= a.N) continue;
                 const int64_t row = ((int64_t)e * a.N + n) * a.K;
+                if (a.out_f32) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int k = k0 + (wn * NT + j) * 16 + (lane >> 4) * 4;
-                    if (k >= a.K) continue;
-                    if (a.out_f32) {
+                    for (int j = 0; j < NT; ++j) {
+                        const int k = k0 + (wn * NT + j) * 16 + (lane >> 4) * 4;
+                        if (n >= a.N || k >= a.K) continue;
                         f32x4 *o = (f32x4 *)((float *)a.out + row + k);
                         *o = a.accumulate ? *o + acc[i][j] : acc[i][j];
-                    } else {
-                        *(u16x4 *)((uint16_t *)a.out + row + k) = u16x4{bf16_of(acc[i][j].x), bf16_of(acc[i][j].y),
-                                                                       bf16_of(acc[i][j].z), bf16_of(acc[i][j].w)};
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NT; j += 4) {
+                        u32x4 v[2];
+                        to_row(acc[i] + j, v);
+                        const int k = k0 + (wn * NT + j + (lane >> 4)) * 16;
+                        if (n < a.N && k < a.K) *(u32x4 *)((uint16_t *)a.out + row + k) = v[0];
+                        if (n < a.N && k + 8 < a.K) *(u32x4 *)((uint16_t *)a.out + row + k + 8) = v[1];
                     }
                 }
             }
