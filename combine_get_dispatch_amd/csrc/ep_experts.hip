@@ -786,8 +786,9 @@ struct WgradArgs {
 // grad_W[e][n][k] = sum over e's rows: both operands are reduction-strided and
 // read through the transposing read. A BM (n) x BN (k) tile, 64 rows a step;
 // rows past the expert's last are zeros on both sides, so that whatever the
-// unused receive rows hold (NaN included) does not enter a sum.
-template <int BM, int BN, int WM, int WN>
+// unused receive rows hold (NaN included) does not enter a sum. REGIONS: the
+// low-latency layout, whose rows are looked up one by one.
+template <int BM, int BN, int WM, int WN, bool REGIONS>
 struct Wgrad {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int ACT = BM / 16 / WM, NT = BN / 16 / WN;
@@ -810,7 +811,7 @@ struct Wgrad {
 
     __device__ __forceinline__ Wgrad(const WgradArgs &a, int e_, int count_, int n0, int k0, int wave_, int lane_)
         : g(&a.g), e(e_), count(count_), wave(wave_), lane(lane_), grow(a.N * 2), xrow(a.K * 2) {
-        const int64_t base = a.g.region_rows > 0 || count == 0 ? 0 : ep::group_row(a.g, e, 0);
+        const int64_t base = REGIONS || count == 0 ? 0 : ep::group_row(a.g, e, 0);
         gb = uniform(a.grad + base * grow + n0 * 2);
         xb = uniform(a.x + base * xrow + k0 * 2);
         // columns past the end repeat the last chunk
@@ -843,8 +844,8 @@ struct Wgrad {
         const int r = (ins * 64 + lane) / ((of_grad ? BM : BN) / 8), m = step * 64 + r;
         const uint8_t *p = (const uint8_t *)&k_zero_chunk;
         if (m < count)
-            p = g->region_rows > 0 ? base + ep::group_row(*g, e, m) * width + (off - (uint32_t)r * width)
-                                   : base + (int64_t)step * 64 * width + off;
+            p = REGIONS ? base + ep::group_row(*g, e, m) * width + (off - (uint32_t)r * width)
+                        : base + (int64_t)step * 64 * width + off;
         copy16(p, to);
     }
     __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
@@ -886,7 +887,7 @@ struct Wgrad {
             if (count > 0) {
                 __syncthreads();  // the last tile's reads of the ring are done
                 reduce(Wgrad(a, e, count, n0, k0, wave, lane), lds_address(sh.ring), (count + 63) / 64,
-                       a.g.region_rows > 0 ? 0 : count / 64, acc);
+                       REGIONS ? 0 : count / 64, acc);
             } else if (a.accumulate) {
                 continue;
             }
@@ -917,9 +918,9 @@ struct Wgrad {
     }
 };
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, bool REGIONS>
 __global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_wgrad(WgradArgs a) {
-    using P = Wgrad<BM, BN, WM, WN>;
+    using P = Wgrad<BM, BN, WM, WN, REGIONS>;
     __shared__ typename P::Shared sh;
     P::body(a, sh);
 }
@@ -959,7 +960,11 @@ template <int BM, int BN, int WM, int WN>
 hipError_t launch_wgrad(const WgradArgs &a, int cus, hipStream_t s) {
     const int64_t tiles = (int64_t)a.g.E * ((a.N + BM - 1) / BM) * ((a.K + BN - 1) / BN);
     const int64_t most = (int64_t)cus * (BN >= 256 ? 1 : 2);
-    k_wgrad<BM, BN, WM, WN><<<(int)(tiles < most ? tiles : most), WM * WN * 64, 0, s>>>(a);
+    const int grid = (int)(tiles < most ? tiles : most);
+    if (a.g.region_rows > 0)
+        k_wgrad<BM, BN, WM, WN, true><<<grid, WM * WN * 64, 0, s>>>(a);
+    else
+        k_wgrad<BM, BN, WM, WN, false><<<grid, WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -1046,9 +1051,12 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     a.N = N;
     a.out_f32 = out_f32 != 0;
     a.accumulate = accumulate != 0;
+    // 256 x 256 tiles where there are enough for the chip and rows enough to sum, else 128 x 128 (48 experts of 7 rows,
+    // 126 MB of fp32 results: TIMEHERE)
     const int64_t big = (int64_t)a.g.E * ((N + 255) / 256) * ((K + 255) / 256);
-    const hipError_t e = big >= cus ? launch_wgrad<256, 256, 2, 2>(a, cus, (hipStream_t)stream)
-                                    : launch_wgrad<128, 128, 2, 2>(a, cus, (hipStream_t)stream);
+    const bool wide = big >= cus && ep::group_rows_expected(groups) >= 128 * (int64_t)a.g.E;
+    const hipError_t e = wide ? launch_wgrad<256, 256, 2, 2>(a, cus, (hipStream_t)stream)
+                              : launch_wgrad<128, 128, 2, 2>(a, cus, (hipStream_t)stream);
     return ep::hip_status(e, "ep_expert_gemm_wgrad");
 }
 

@@ -85,9 +85,11 @@ struct RowWalk {
 enum Op { kSwigluBf16, kSwigluFp8, kSwigluMx4, kSwigluGrad, kQuantize, kDequantize };
 
 constexpr int kPer = 8;     // channels per lane and chunk
-// chunks whose loads are in flight together: SwiGLU's gradient 260 us with 4, 267 with 2; MXFP4 there and back 155 and 129
-template <int OP>
-constexpr int kUnroll = OP == kQuantize || OP == kDequantize ? 2 : 4;
+constexpr int kUnroll = 2;      // chunks whose loads are in flight together
+// Workgroups per CU at most, eight of which are resident: with 8, whose waves
+// share all chunks out among them, SwiGLU's gradient took 260 us and MXFP4
+// there and back 129, with 64 (and the hardware dealing them out) 233 and 119.
+constexpr int kBlocksPerCu = 64;
 
 // 16-byte vectors that a lane loads
 template <int OP>
@@ -236,7 +238,7 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
 
 template <int OP>
 __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs a) {
-    constexpr int U = kUnroll<OP>;
+    constexpr int U = kUnroll;
     __shared__ int ends[ep::kGroupsMaxExperts];
     const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
     const int lane = threadIdx.x & 63;
@@ -276,7 +278,7 @@ template <int OP>
 hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
     const int64_t chunks = (a.cols + 64 * kPer - 1) / (64 * kPer);
     const int64_t blocks = (rows * chunks + kThreads / 64 - 1) / (kThreads / 64);
-    const int64_t most = (int64_t)cus * 8;
+    const int64_t most = (int64_t)cus * kBlocksPerCu;
     k_rows<OP><<<(int)(blocks < 1 ? 1 : blocks < most ? blocks : most), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
