@@ -286,7 +286,7 @@ hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) 
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 // common checks of the row-wise calls; EP_OK with *rows = 0: nothing to do
-int rows_args(const ep_groups *groups, int64_t num_rows, int64_t cols, RowsArgs *a, int64_t *rows, int *cus) {
+int rows_args(const ep_groups *groups, int64_t num_rows, int64_t cols, RowsArgs *a, int64_t *rows) {
     a->grouped = groups != nullptr;
     a->num_rows = num_rows;
     a->cols = cols;
@@ -302,7 +302,7 @@ int rows_args(const ep_groups *groups, int64_t num_rows, int64_t cols, RowsArgs 
         const int64_t n = ep::group_rows_expected(groups);
         *rows = num_rows == 0 ? 0 : n < 1 ? 1 : n;
     }
-    return *rows ? ep::device_cus(cus) : EP_OK;
+    return EP_OK;
 }
 
 }  // namespace
@@ -372,11 +372,12 @@ int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows
     int cus = 0;
     if (form != EP_FORM_BF16 && form != EP_FORM_FP8 && form != EP_FORM_MXFP4) return EP_ERR_ARG;
     if (I < 8 || I > 65536 || I % (form == EP_FORM_BF16 ? 8 : form == EP_FORM_FP8 ? 128 : 32)) return EP_ERR_ARG;
-    if (int r = rows_args(groups, num_rows, I, &a, &rows, &cus)) return r;
+    if (int r = rows_args(groups, num_rows, I, &a, &rows)) return r;
     if (rows == 0) return EP_OK;
     if (!gate_up || !out || (form != EP_FORM_BF16) != (scales != nullptr)) return EP_ERR_ARG;
     if (misaligned(gate_up, 16) || misaligned(out, 16) || misaligned(scales, form == EP_FORM_FP8 ? 4 : 1))
         return EP_ERR_ALIGN;
+    if (int r = ep::device_cus(&cus)) return r;
     a.a = gate_up;
     a.out = out;
     a.scales = scales;
@@ -393,10 +394,11 @@ int ep_swiglu_backward(const ep_groups *groups, const uint16_t *grad_out, const 
     int64_t rows;
     int cus = 0;
     if (I < 8 || I > 65536 || I % 8) return EP_ERR_ARG;
-    if (int r = rows_args(groups, num_rows, I, &a, &rows, &cus)) return r;
+    if (int r = rows_args(groups, num_rows, I, &a, &rows)) return r;
     if (rows == 0) return EP_OK;
     if (!grad_out || !gate_up || !grad_gate_up) return EP_ERR_ARG;
     if (misaligned(grad_out, 16) || misaligned(gate_up, 16) || misaligned(grad_gate_up, 16)) return EP_ERR_ALIGN;
+    if (int r = ep::device_cus(&cus)) return r;
     a.a = gate_up;
     a.d = grad_out;
     a.out = grad_gate_up;
@@ -409,10 +411,11 @@ int ep_quantize_mxfp4(const ep_groups *groups, const uint16_t *x, int64_t num_ro
     int64_t rows;
     int cus = 0;
     if (cols < 32 || cols > 65536 || cols % 32) return EP_ERR_ARG;
-    if (int r = rows_args(groups, num_rows, cols, &a, &rows, &cus)) return r;
+    if (int r = rows_args(groups, num_rows, cols, &a, &rows)) return r;
     if (rows == 0) return EP_OK;
     if (!x || !q || !scales) return EP_ERR_ARG;
     if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    if (int r = ep::device_cus(&cus)) return r;
     if (!groups) {  // dense rows are one long one
         a.cols = num_rows * cols;
         a.num_rows = rows = 1;
@@ -429,10 +432,11 @@ int ep_dequantize_mxfp4(const ep_groups *groups, const uint8_t *q, const uint8_t
     int64_t rows;
     int cus = 0;
     if (cols < 32 || cols > 65536 || cols % 32) return EP_ERR_ARG;
-    if (int r = rows_args(groups, num_rows, cols, &a, &rows, &cus)) return r;
+    if (int r = rows_args(groups, num_rows, cols, &a, &rows)) return r;
     if (rows == 0) return EP_OK;
     if (!x || !q || !scales) return EP_ERR_ARG;
     if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    if (int r = ep::device_cus(&cus)) return r;
     if (!groups) {
         a.cols = num_rows * cols;
         a.num_rows = rows = 1;

@@ -442,7 +442,8 @@ int ep_pattern_gather(const uint16_t *rows, const int32_t *pos, uint16_t *out, i
  * the same data gives the same bits.
  * Limits: 1 <= num_experts <= 1024, 1 <= num_ranks <= 64, num_experts %
  * num_ranks == 0, num_ranks*cap_rows < 2^31; 8 <= channels <= 65536,
- * channels % 8 == 0 (% 128 along the reduction of FP8 and MXFP4 products). */
+ * channels % 8 == 0 (% 128 along the reduction of FP8 and MXFP4 products); an
+ * expert's regions together under 4 GiB of a product's rows. */
 typedef struct {
     const int32_t *offsets; /* [E], or NULL with region_rows > 0 */
     const int32_t *counts;  /* [E], or [E][R] with region_rows > 0 */
@@ -471,7 +472,8 @@ typedef struct {
  *   MXFP4: rows [R*cap_rows][K/2] and weights [E][N][K/2] bytes with scales
  *     [..][K/32] bytes, a scale byte b standing for 2^(b-127), 255 for NaN
  *     (ep_quantize_mxfp4 writes both).
- * out: [R*cap_rows][N]. Rows, weights and out 16-byte aligned, scales 4-byte. */
+ * out: [R*cap_rows][N]; it overlaps no input. Rows, weights, out and MXFP4
+ * scales 16-byte aligned, FP8 scales 4-byte. */
 int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const void *row_scales, const void *weights,
                    const void *weight_scales, int K, int N, uint16_t *out, ep_stream_t stream);
 
