@@ -27,6 +27,14 @@ current stream, and the outputs are caller-owned tensors)::
     grad_x = buf.dispatch_backward(grad_expert_in, handle, topk_w)
     assert buf.status() == 0                               # sticky device status
 
+The experts' own computation on the received rows (FP8 rows and weights here;
+bf16 and MXFP4 likewise, and the bf16 gradients)::
+
+    g = buf.groups(layout)                                 # low-latency: buf.groups_low_latency(recv_count)
+    h = ep.expert_gemm(recv_x, w13, g, row_scales=recv_scales, weight_scales=s13)   # [rows, 2I] bf16
+    a, a_scales = ep.swiglu(h, g, kind="fp8")
+    expert_out = ep.expert_gemm(a, w2, g, row_scales=a_scales, weight_scales=s2)
+
 The rank-deduplicated exchange (``dispatch_dedup_with_layout``: one row per
 (token, destination rank) with the row's local expert indices and weights)
 and the low-latency form (``dispatch_low_latency``: fixed per-(expert,

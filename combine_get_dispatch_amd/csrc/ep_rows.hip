@@ -7,6 +7,10 @@
 // whole scale group, took 2.3 times as long to write), a run of neighbouring
 // chunks per wave, kUnroll chunks' loads in flight together. A scale group of
 // 32 channels is four lanes, one of 128 sixteen.
+//
+// On MI355X: SwiGLU of 32768 rows x 2048 to FP8 71 us (338 MB, 4.8 TB/s), its
+// gradient on 65536 rows 234 us (1.34 GB, 5.7 TB/s), 16384 x 7168 values to
+// MXFP4 55 us and back 64 us (297 MB each, 5.4 and 4.6 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
