@@ -80,29 +80,38 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
 // compiler, which cannot tell the ring's buffers apart, otherwise waits for
 // all copies in flight before every LDS read; the instruction has no result
 // register, and the waits are wait_copies() below. M0 holds the LDS address
-// and needs one wait state before its use.
+// and needs one wait state before its use; a base that a vector instruction
+// wrote needs five, which no place in the compiled kernels falls short of (a
+// test reads them).
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 // the same for bytes that nothing reads again: they take no other line's place in the caches
 __device__ __forceinline__ void copy16_once(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 // the same with an address per lane
 __device__ __forceinline__ void copy16(const uint8_t *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
 }
 
 // Wait until at most `N` of this wave's copies are in flight and its LDS
@@ -284,12 +293,16 @@ enum Copies { kLast, kWhole, kPartial };
 // the first `whole` of which need no check for the end of the rows. A step is
 // two halves of 64 bytes per row. While one half's matrix instructions run,
 // the next half's fragments are read into registers (and the MXFP4 form's
-// scales with them), and the copies of the step kStages ahead are issued; the workgroup meets once a step, in its
-// middle, when the step's buffer has been read out and the next one's must
-// have landed. The order of the source is kept (pin): a few matrix
+// scales with them); the workgroup meets once a step, in its middle, when the
+// step's buffer has been read out and the next one's must have landed; in the
+// second half the copies of the step kStages ahead follow, evenly (all at its
+// start they queue: 3315 us against 2998 for both gradients of 32768 rows, 8
+// experts of 4096 x 7168). The order of the source is kept (pin): a few matrix
 // instructions, then a read or a copy, and so on, so that the matrix unit
 // always has work queued. (The last step reads a next one that is none;
-// nothing uses it.)
+// nothing uses it.) 16 x 16 matrix instructions, not 32 x 32: those take 4%
+// fewer cycles, but move twice the accumulators per product, and the clock
+// under them falls further (3245 us).
 template <class P>
 __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
     constexpr int ACT = P::ACT, NT = P::NT, S = P::kStages;
@@ -434,7 +447,7 @@ struct HalfFrags {
 // with few rows costs each of them as little, in steps of half, a quarter, an
 // eighth (ACT row tiles per wave), of rows copied as well as multiplied.
 //
-// Scales are copied in runs of several steps, 16 or 32 bytes per row, where
+// Scales are copied in runs of several steps, 16 bytes per row, where
 // their rows allow it (RUNS: K % 512 == 0): a copy instruction takes a cycle
 // or more per memory line its lanes touch, and every row of the scales is
 // another line. (Step by step they cost 12% of a 256 x 256 tile's time.)

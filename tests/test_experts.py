@@ -168,11 +168,13 @@ def test_matrix_instructions_written_as_asm(tmp_path):
     """The compiler keeps the distances that matrix instructions need between
     each other and other instructions, except for those written as asm: no
     vector instruction may write one of their operands in the two wait states
-    before, and nothing else may touch their results in the 18 after."""
+    before, and nothing else may touch their results in the 18 after. The same
+    for the copies to LDS: a vector instruction writes the scalar registers of
+    their base no later than five wait states before."""
     out = str(tmp_path / "experts.s")
     subprocess.run([epbuild.hipcc()] + epbuild.flags() + ["-S", "--offload-device-only", "-o", out,
                    os.path.join(epbuild.CSRC, "ep_experts.hip")], check=True, capture_output=True)
-    seen, window, in_asm = 0, [], False
+    seen, copies, window, in_asm = 0, 0, [], False
     for line in open(out):
         t = line.strip()
         if t.startswith(";;#ASM"):
@@ -194,11 +196,19 @@ def test_matrix_instructions_written_as_asm(tmp_path):
                 late = [w for kind, w, ago in window if kind == "valu" and ago < 2 and w & read]
                 assert not late, f"operand written right before: {t}"
                 entry = ("asm", registers(operands[0]), 0)
+        elif op.startswith("global_load_lds"):
+            copies += 1
+            base = {f"s{i}" for lo, hi in re.findall(r"\bs\[(\d+):(\d+)\]", rest) for i in range(int(lo), int(hi) + 1)}
+            late = [w for kind, w, ago in window if kind == "scalar" and ago < 5 and w & base]
+            assert not late, f"base written right before: {t}"
         elif op.startswith(("v_", "global_", "ds_", "scratch_", "buffer_")):
             touched = registers(rest)
             early = [w for kind, w, ago in window if kind == "asm" and ago < 18 and w & touched]
             assert not early, f"result touched too early: {t}"
+            scalar = {f"s{i}" for i in re.findall(r"\bs(\d+)\b", operands[0])}
+            scalar |= {f"s{i}" for lo, hi in re.findall(r"\bs\[(\d+):(\d+)\]", operands[0])
+                       for i in range(int(lo), int(hi) + 1)}
             if op.startswith("v_"):
-                entry = ("valu", registers(operands[0]), 0)
+                entry = ("scalar", scalar, 0) if scalar else ("valu", registers(operands[0]), 0)
         window = [(k, w, ago + states) for k, w, ago in window if ago + states < 18] + ([entry] if entry else [])
-    assert seen > 1000  # (there are some)
+    assert seen > 1000 and copies > 1000  # (there are some)
