@@ -357,3 +357,31 @@ def test_expert_counts(E):
         ref = ov[rows[e]].t() @ x.double()[rows[e]]
         mag = ov[rows[e]].abs().t() @ x.double()[rows[e]].abs()
         near(gw[e], ref, 12 * 2.0 ** -23 * mag + 2.0 ** -24 * ref.abs(), "wgrad")
+
+
+@pytest.mark.parametrize("form", ["bf16", "fp8", "mxfp4"])
+def test_same_bits_again_and_on_few_compute_units(form):
+    """A call repeated, and made on a stream that may use 32 compute units, gives the same bits; any hint the right result."""
+    rng = np.random.default_rng(20)
+    E, K, N = 8, 1024, 640
+    off, cap, rows = xh.packed_groups([300, 0, 17, 256, 90, 1, 513, 64], 2)
+    counts = torch.tensor([len(r) for r in rows], dtype=torch.int32).cuda()
+    x, xs = (t if t is None else t.cuda() for t in xh.make_operand(rng, (2 * cap, K), form))
+    w, ws = (t if t is None else t.cuda() for t in xh.make_operand(rng, (E, N, K), form, weights=True))
+
+    def call(hint):
+        g = ep.Groups(counts, torch.from_numpy(off).cuda(), num_experts=E, num_ranks=2, cap_rows=cap, rows_hint=hint)
+        out = torch.zeros((2 * cap, N), dtype=torch.bfloat16, device="cuda")
+        return ep.expert_gemm(x, w, g, row_scales=xs, weight_scales=ws, out=out)
+
+    first = call(0)
+    assert torch.equal(call(0), first)
+    torch.cuda.synchronize()
+    with ep.CuStream(32) as s, torch.cuda.stream(s.torch_stream):
+        capped = call(0)
+        s.torch_stream.synchronize()
+    assert torch.equal(capped, first)
+    for hint in (1, 8 * 40, 1 << 20):
+        check_product(call(hint), xh.operand(*(t if t is None else t.cpu() for t in (x, xs)), form),
+                      xh.operand(*(t if t is None else t.cpu() for t in (w, ws)), form, True),
+                      [torch.tensor(r, dtype=torch.long) for r in rows], form, f"hint {hint}")
