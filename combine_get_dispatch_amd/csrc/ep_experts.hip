@@ -360,11 +360,11 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
     f32x4 part[2][NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        w[j] = join(p.w(ring, j, 0), p.w(ring, j, 1));
+        w[j] = P::w_whole(p.w_base(ring, 0), p.w_base(ring, 1), j);
         part[1][j] = f32x4{0, 0, 0, 0};
     }
-    x[0] = join(p.x(ring, 0, 0), p.x(ring, 0, 1));
-    float s_next = p.x_scale(ring, 0, 0), f = 0.0f, f_prev = 0.0f;  // times 0: there is no tile before the first
+    x[0] = P::x_whole(p.x_base(ring, 0), p.x_base(ring, 1), 0);
+    float s_next = P::x_scale(p.scale_base(ring, 0), 0), f = 0.0f, f_prev = 0.0f;  // times 0: there is no tile before the first
     float ws = w_scales[0];
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
@@ -376,6 +376,8 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
         constexpr int SOON = P::kSoon, LATE = P::kPer - SOON, L = ACT * NT >= 8 ? ACT * NT * 3 / 8 : ACT * NT;
         if (COPIES == kLast && step + S - 1 < steps) copy_step(p, pv, step + S - 1, steps, SOON, P::kPer);
         const float ws_next = w_scales[step + 1 < steps ? step + 1 : step];
+        const uint32_t x0 = p.x_base(st, 0), x1 = p.x_base(st, 1), nx0 = p.x_base(nx, 0), nx1 = p.x_base(nx, 1);
+        const uint32_t w0 = p.w_base(nx, 0), w1 = p.w_base(nx, 1), xs = p.scale_base(st, step);
 #pragma unroll
         for (int i = 0; i < ACT; ++i) {
             const bool last = i == ACT - 1;
@@ -385,11 +387,11 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
             f_prev = f;
             f = s_next * ws;
             if (!last) {
-                x[(i + 1) & 1] = join(p.x(st, i + 1, 0), p.x(st, i + 1, 1));
-                s_next = p.x_scale(st, step, i + 1);
+                x[(i + 1) & 1] = P::x_whole(x0, x1, i + 1);
+                s_next = P::x_scale(xs, i + 1);
             } else {
-                s_next = p.x_scale(nx, step + 1, 0);
-                if (ACT > 1) x[0] = join(p.x(nx, 0, 0), p.x(nx, 0, 1));
+                s_next = P::x_scale(p.scale_base(nx, step + 1), 0);
+                if (ACT > 1) x[0] = P::x_whole(nx0, nx1, 0);
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -404,7 +406,7 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
 #pragma unroll
                     for (int c = j * SOON / NT; c < (j + 1) * SOON / NT; ++c)
                         if (COPIES == kWhole) p.template copy<true>(step + S, st, c);
-                    w[j] = join(p.w(nx, j, 0), p.w(nx, j, 1));
+                    w[j] = P::w_whole(w0, w1, j);
                 }
                 const int to = (i + ACT - 1) % ACT;
                 if (ACT > 1) {
@@ -416,7 +418,7 @@ __device__ __forceinline__ void reduce_fp8(const P &p, uint32_t ring, int steps,
                 }
                 pin();
             }
-            if (ACT == 1) x[0] = join(p.x(nx, 0, 0), p.x(nx, 0, 1));
+            if (ACT == 1) x[0] = P::x_whole(nx0, nx1, 0);
         }
         ws = ws_next;
         ++step;
@@ -636,6 +638,17 @@ struct Product {
             copy_run(0, 1);
         }
 
+        // where a buffer's fragments of half s begin for this lane: one sum a buffer, the tiles' offsets constants
+        __device__ __forceinline__ uint32_t x_base(uint32_t stage, int s) const { return stage + xr + half[s]; }
+        __device__ __forceinline__ uint32_t w_base(uint32_t stage, int s) const { return stage + wr + half[s]; }
+        static __device__ __forceinline__ i32x8 x_whole(uint32_t a, uint32_t b, int i) {
+            const uint32_t at = i * WM * 16 * kStepBytes;
+            return join(lds_read<i32x4>(a + at), lds_read<i32x4>(b + at));
+        }
+        static __device__ __forceinline__ i32x8 w_whole(uint32_t a, uint32_t b, int j) {
+            const uint32_t at = j * 16 * kStepBytes;
+            return join(lds_read<i32x4>(a + at), lds_read<i32x4>(b + at));
+        }
         __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
             return lds_read<i32x4>(stage + xr + half[s] + i * WM * 16 * kStepBytes);
         }
@@ -643,10 +656,13 @@ struct Product {
             if constexpr (WTR) return read_tr<BN>(stage + kXBytes, wave % WN * NT + j, s);
             return lds_read<i32x4>(stage + wr + half[s] + j * 16 * kStepBytes);
         }
-        __device__ __forceinline__ float x_scale(uint32_t stage, int step, int i) const {
-            const int row = (wave / WN + i * WM) * 16 + (lane & 15);
-            return RUNS ? lds_read<float>(scales + step / kRun % 3 * kXsRun + row * 16 + step % kRun * 4)
-                        : lds_read<float>(stage + kXBytes + kWBytes + row * 4);
+        // the same of the row tiles' FP8 scales
+        __device__ __forceinline__ uint32_t scale_base(uint32_t stage, int step) const {
+            const uint32_t row = wave / WN * 16 + (lane & 15);
+            return RUNS ? scales + step / kRun % 3 * kXsRun + step % kRun * 4 + row * 16 : stage + kXBytes + kWBytes + row * 4;
+        }
+        static __device__ __forceinline__ float x_scale(uint32_t base, int i) {
+            return lds_read<float>(base + i * WM * 16 * (RUNS ? 16 : 4));
         }
         // the f-th read of half s: the weights' fragments (and scales), then the rows'
         __device__ __forceinline__ void read(Frags &h, uint32_t stage, int step, int f, int s) const {
