@@ -18,7 +18,7 @@
 // 128 x 64). 128 x 128, two workgroups per CU, where an expert has few rows
 // and the weights' bytes are the time. On MI355X: gradients of 32768 rows, 8
 // experts of 4096 x 7168: 1.28 PFLOP/s (a library product of that size 1.52);
-// FP8, 32768 rows on 8 experts of the same size: 2.15 PFLOP/s (2.94); MXFP4,
+// FP8, 32768 rows on 8 experts of the same size: 2.27 PFLOP/s (2.94); MXFP4,
 // 16384 rows: 3.8 PFLOP/s; 1024 rows on 256 experts, 7.4 GB of FP8 weights:
 // 1090 us, 6.8 TB/s. What bounds the large ones: bf16 the clock under matrix
 // instructions; FP8 the issue of one scale addition per result and 128
@@ -309,7 +309,7 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
     fill_ring(p, ring, steps, whole);
     typename P::Frags h0, h1;
 #pragma unroll
-    for (int f = 0; f < P::kReads; ++f) p.read(h0, ring, 0, f, 0);
+    for (int f = 0; f < P::kReads; ++f) p.read(h0, p.place(ring, 0, 0), f);
     int slot = 0, step = 0;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
@@ -317,10 +317,11 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
         const uint32_t st = ring + slot * P::kStage;
         slot = slot + 1 == S ? 0 : slot + 1;
         const uint32_t nx = ring + slot * P::kStage;
+        const auto half = p.place(st, step, 1), next = p.place(nx, step + 1, 0);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
 #pragma unroll
-            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h1, st, step, f, 1);
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h1, half, f);
             p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
@@ -331,7 +332,7 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
             for (int f = (m + H) * C / M; f < (m + 1 + H) * C / M && f < C; ++f)  // between the reads
                 if (COPIES != kLast) p.template copy<COPIES == kWhole>(step + S, st, f);
 #pragma unroll
-            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h0, nx, step + 1, f, 0);
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h0, next, f);
             p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }
@@ -649,13 +650,6 @@ struct Product {
             const uint32_t at = j * 16 * kStepBytes;
             return join(lds_read<i32x4>(a + at), lds_read<i32x4>(b + at));
         }
-        __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
-            return lds_read<i32x4>(stage + xr + half[s] + i * WM * 16 * kStepBytes);
-        }
-        __device__ __forceinline__ i32x4 w(uint32_t stage, int j, int s) const {
-            if constexpr (WTR) return read_tr<BN>(stage + kXBytes, wave % WN * NT + j, s);
-            return lds_read<i32x4>(stage + wr + half[s] + j * 16 * kStepBytes);
-        }
         // the same of the row tiles' FP8 scales
         __device__ __forceinline__ uint32_t scale_base(uint32_t stage, int step) const {
             const uint32_t row = wave / WN * 16 + (lane & 15);
@@ -664,24 +658,33 @@ struct Product {
         static __device__ __forceinline__ float x_scale(uint32_t base, int i) {
             return lds_read<float>(base + i * WM * 16 * (RUNS ? 16 : 4));
         }
-        // the f-th read of half s: the weights' fragments (and scales), then the rows'
-        __device__ __forceinline__ void read(Frags &h, uint32_t stage, int step, int f, int s) const {
-            if constexpr (FORM == kMx4) {
+        struct Half {
+            uint32_t x, w, xs, stage;
+            int s;
+        };
+        __device__ __forceinline__ Half place(uint32_t stage, int step, int s) const {
+            Half h = {x_base(stage, s), w_base(stage, s), 0, stage, s};
+            if constexpr (FORM == kMx4)
+                h.xs = (RUNS ? scales + step / 2 % 3 * (kXsRun + kWsRun) + step % 2 * 8 : stage + kXBytes + kWBytes) +
+                       (wave / WN * 16 + (lane & 15)) * (RUNS ? 16 : 8) + (lane >> 4) * 2 + s;
+            return h;
+        }
+        // the f-th read of a half: the weights' fragments (and scales), then the rows'
+        __device__ __forceinline__ void read(Frags &h, const Half &at, int f) const {
+            const int i = FORM == kMx4 ? f / 2 : f;
+            if (FORM == kMx4 && f % 2 == 1) {
                 constexpr int kRow = RUNS ? 16 : 8;
-                const int i = f / 2;
-                const uint32_t own = (lane & 15) * kRow + (lane >> 4) * 2 + s;
-                const uint32_t xs = (RUNS ? scales + step / 2 % 3 * (kXsRun + kWsRun) + step % 2 * 8
-                                          : stage + kXBytes + kWBytes) + own;
-                const uint32_t ws = xs + (RUNS ? kXsRun : kXScale);
-                if (f % 2 == 0 && i < NT) h.w[i] = w(stage, i, s);
-                if (f % 2 == 1 && i < NT) h.ws[i] = lds_read<uint8_t>(ws + (wave % WN * NT + i) * 16 * kRow);
-                if (f % 2 == 0 && i >= NT) h.x[i - NT] = x(stage, i - NT, s);
-                if (f % 2 == 1 && i >= NT) h.xs[i - NT] = lds_read<uint8_t>(xs + (wave / WN + (i - NT) * WM) * 16 * kRow);
-            } else {
-                if (f < NT)
-                    h.w[f] = w(stage, f, s);
+                if (i < NT)
+                    h.ws[i] = lds_read<uint8_t>(at.xs + (RUNS ? kXsRun : kXScale) + (wave % WN * NT - wave / WN + i) * 16 * kRow);
                 else
-                    h.x[f - NT] = x(stage, f - NT, s);
+                    h.xs[i - NT] = lds_read<uint8_t>(at.xs + (i - NT) * WM * 16 * kRow);
+            } else if (i < NT) {
+                if constexpr (WTR)
+                    h.w[i] = read_tr<BN>(at.stage + kXBytes, wave % WN * NT + i, at.s);
+                else
+                    h.w[i] = lds_read<i32x4>(at.w + i * 16 * kStepBytes);
+            } else {
+                h.x[i - NT] = lds_read<i32x4>(at.x + (i - NT) * WM * 16 * kStepBytes);
             }
         }
         __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
@@ -889,18 +892,17 @@ struct Wgrad {
                         : base + (int64_t)step * 64 * width + off;
         copy16(p, to);
     }
-    __device__ __forceinline__ i32x4 x(uint32_t stage, int i, int s) const {
-        return read_tr<BM>(stage, wave / WN + i * WM, s);
-    }
-    __device__ __forceinline__ i32x4 w(uint32_t stage, int j, int s) const {
-        return read_tr<BN>(stage + kGBytes, wave % WN * NT + j, s);
-    }
     __device__ __forceinline__ void first_run() const {}
-    __device__ __forceinline__ void read(Frags &h, uint32_t stage, int, int f, int s) const {
+    struct Half {
+        uint32_t stage;
+        int s;
+    };
+    __device__ __forceinline__ Half place(uint32_t stage, int, int s) const { return {stage, s}; }
+    __device__ __forceinline__ void read(Frags &h, const Half &at, int f) const {
         if (f < NT)
-            h.w[f] = w(stage, f, s);
+            h.w[f] = read_tr<BN>(at.stage + kGBytes, wave % WN * NT + f, at.s);
         else
-            h.x[f - NT] = x(stage, f - NT, s);
+            h.x[f - NT] = read_tr<BM>(at.stage, wave / WN + (f - NT) * WM, at.s);
     }
     __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
         mfma_bf16<kAcc>(h.w[j], h.x[i], c);
