@@ -57,12 +57,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // error stays near that of the hardware's exp2 and reciprocal (one step each)
 // for large |g| too. A result below 2^-126 (g below -87) is 0: the hardware's
 // reciprocal has no subnormal results, and silu that small is none to keep.
+// r is left out for |t| >= 128, where exp2 is infinite or nothing beside 1:
+// from |g| = 2.36e38 on t is infinite and r no number.
 __device__ __forceinline__ float sigmoid(float g) {
     constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596299112661746887e-8f;
     const float t = -g * kLog2e;
     const float r = fmaf(-g, kLog2e, -t) - g * kRest;
     const float x = __builtin_amdgcn_exp2f(t);
-    const float y = x < 3.0e38f ? fmaf(x, r * 0.693147180559945309f, x) : x;  // no inf - inf
+    const float y = fabsf(t) < 128.0f ? fmaf(x, r * 0.693147180559945309f, x) : x;  // (NaN: x)
     return __builtin_amdgcn_rcpf(1.0f + y);
 }
 
