@@ -1034,7 +1034,14 @@ int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const vo
     if (misaligned(rows, 16) || misaligned(weights, 16) || misaligned(out, 16) || misaligned(row_scales, scale_align) ||
         misaligned(weight_scales, scale_align))
         return EP_ERR_ALIGN;
-    if (far_regions(a.g, form == EP_FORM_BF16 ? K * 2 : form == EP_FORM_FP8 ? K : K / 2)) return EP_ERR_ARG;
+    const int64_t all = ep::group_rows(groups), E = a.g.E;
+    const int64_t width = form == EP_FORM_BF16 ? K * 2 : form == EP_FORM_FP8 ? K : K / 2;
+    if (far_regions(a.g, (int)width)) return EP_ERR_ARG;
+    const int64_t per_row = form == EP_FORM_FP8 ? K / 128 * 4 : K / 32, out_bytes = all * N * 2;  // a row's scales
+    if (ep::overlap(out, out_bytes, rows, all * width) || ep::overlap(out, out_bytes, weights, E * N * width) ||
+        ep::overlap(out, out_bytes, row_scales, all * per_row) ||
+        ep::overlap(out, out_bytes, weight_scales, E * (form == EP_FORM_FP8 ? (N + 127) / 128 : N) * per_row))
+        return EP_ERR_ARG;
     int cus;
     if (int r = ep::device_cus(&cus)) return r;
     a.x = (const uint8_t *)rows;
@@ -1066,6 +1073,10 @@ int ep_expert_gemm_dgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     if (!grad_out || !weights || !grad_rows) return EP_ERR_ARG;
     if (misaligned(grad_out, 16) || misaligned(weights, 16) || misaligned(grad_rows, 16)) return EP_ERR_ALIGN;
     if (far_regions(a.g, N * 2)) return EP_ERR_ARG;
+    const int64_t all = ep::group_rows(groups);
+    if (ep::overlap(grad_rows, all * K * 2, grad_out, all * N * 2) ||
+        ep::overlap(grad_rows, all * K * 2, weights, (int64_t)a.g.E * N * K * 2))
+        return EP_ERR_ARG;
     int cus;
     if (int r = ep::device_cus(&cus)) return r;
     a.x = (const uint8_t *)grad_out;
@@ -1088,6 +1099,10 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     if (!grad_weights) return EP_ERR_ARG;
     if (ep::group_rows(groups) > 0 && (!grad_out || !rows)) return EP_ERR_ARG;
     if (misaligned(grad_out, 16) || misaligned(rows, 16) || misaligned(grad_weights, 16)) return EP_ERR_ALIGN;
+    const int64_t all = ep::group_rows(groups), out_bytes = (int64_t)a.g.E * N * K * (out_f32 ? 4 : 2);
+    if (ep::overlap(grad_weights, out_bytes, grad_out, all * N * 2) ||
+        ep::overlap(grad_weights, out_bytes, rows, all * K * 2))
+        return EP_ERR_ARG;
     int cus;
     if (int r = ep::device_cus(&cus)) return r;
     a.x = (const uint8_t *)rows;

@@ -383,6 +383,11 @@ int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows
     if (!gate_up || !out || (form != EP_FORM_BF16) != (scales != nullptr)) return EP_ERR_ARG;
     if (misaligned(gate_up, 16) || misaligned(out, 16) || misaligned(scales, form == EP_FORM_FP8 ? 4 : 1))
         return EP_ERR_ALIGN;
+    const int64_t n = num_rows * I, out_bytes = form == EP_FORM_BF16 ? n * 2 : form == EP_FORM_FP8 ? n : n / 2;
+    const int64_t scale_bytes = form == EP_FORM_FP8 ? n / 128 * 4 : n / 32;
+    if (ep::overlap(out, out_bytes, gate_up, n * 4) || ep::overlap(scales, scale_bytes, gate_up, n * 4) ||
+        ep::overlap(out, out_bytes, scales, scale_bytes))
+        return EP_ERR_ARG;
     if (int r = ep::device_cus(&cus)) return r;
     a.a = gate_up;
     a.out = out;
@@ -404,6 +409,10 @@ int ep_swiglu_backward(const ep_groups *groups, const uint16_t *grad_out, const 
     if (rows == 0) return EP_OK;
     if (!grad_out || !gate_up || !grad_gate_up) return EP_ERR_ARG;
     if (misaligned(grad_out, 16) || misaligned(gate_up, 16) || misaligned(grad_gate_up, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * I;  // in place every lane writes what it read alone
+    if (ep::overlap(grad_gate_up, n * 4, grad_out, n * 2) ||
+        (grad_gate_up != gate_up && ep::overlap(grad_gate_up, n * 4, gate_up, n * 4)))
+        return EP_ERR_ARG;
     if (int r = ep::device_cus(&cus)) return r;
     a.a = gate_up;
     a.d = grad_out;
@@ -421,6 +430,9 @@ int ep_quantize_mxfp4(const ep_groups *groups, const uint16_t *x, int64_t num_ro
     if (rows == 0) return EP_OK;
     if (!x || !q || !scales) return EP_ERR_ARG;
     if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * cols;
+    if (ep::overlap(q, n / 2, x, n * 2) || ep::overlap(scales, n / 32, x, n * 2) || ep::overlap(q, n / 2, scales, n / 32))
+        return EP_ERR_ARG;
     if (int r = ep::device_cus(&cus)) return r;
     if (!groups) {  // dense rows are one long one
         a.cols = num_rows * cols;
@@ -442,6 +454,8 @@ int ep_dequantize_mxfp4(const ep_groups *groups, const uint8_t *q, const uint8_t
     if (rows == 0) return EP_OK;
     if (!x || !q || !scales) return EP_ERR_ARG;
     if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * cols;
+    if (ep::overlap(x, n * 2, q, n / 2) || ep::overlap(x, n * 2, scales, n / 32)) return EP_ERR_ARG;
     if (int r = ep::device_cus(&cus)) return r;
     if (!groups) {
         a.cols = num_rows * cols;

@@ -418,7 +418,9 @@ int ep_pattern_gather(const uint16_t *rows, const int32_t *pos, uint16_t *out, i
  * dispatch and the combine. These calls take no context and no workspace, and
  * allocate nothing: any number may run at once, on any streams, and each may
  * be captured in a HIP graph. They run on the current device, whose memory
- * all their pointers must be.
+ * all their pointers must be. No output may share memory with an input or with
+ * another output of the call (EP_ERR_ARG; arrays count whole, unused rows
+ * among them): only ep_swiglu_backward's may be an input itself.
  *
  * ep_groups says which receive rows are whose (a host struct; the counts and
  * offsets stay on the device and are read when the call runs):
@@ -472,7 +474,7 @@ typedef struct {
  *   MXFP4: rows [R*cap_rows][K/2] and weights [E][N][K/2] bytes with scales
  *     [..][K/32] bytes, a scale byte b standing for 2^(b-127), 255 for NaN
  *     (ep_quantize_mxfp4 writes both).
- * out: [R*cap_rows][N]; it overlaps no input. Rows, weights, out and MXFP4
+ * out: [R*cap_rows][N]. Rows, weights, out and MXFP4
  * scales 16-byte aligned, FP8 scales 4-byte. */
 int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const void *row_scales, const void *weights,
                    const void *weight_scales, int K, int N, uint16_t *out, ep_stream_t stream);

@@ -78,3 +78,60 @@ def test_groups_past_32_bits(as_if_on_gpu, field):
     with pytest.MonkeyPatch.context() as m:
         m.setattr(torch.Tensor, "is_contiguous", lambda t: True)
         assert code_of(g.c) == ep.EP_ERR_ARG
+
+
+# Every output on an input's first and last 16 bytes, and on another output's. (Sizes: 128 rows, 8 experts, K = 256 and N = 64
+# channels.) The arrays' places are never touched: every call is refused.
+ROWS, E, K, N = 128, 8, 256, 64
+BASE = 1 << 40
+
+
+def overlapping(arrays, outputs):
+    """Places {name: address} 1 GiB apart but for one output, which overlaps another array by 16 bytes on either side."""
+    for o in outputs:
+        for other in arrays:
+            if other != o:
+                for side in (0, 1):
+                    at = {n: BASE + (i << 30) for i, n in enumerate(arrays)}
+                    at[o] = at[other] - arrays[o] + 16 if side else at[other] + arrays[other] - 16
+                    yield f"{o} on {other}", at
+
+
+@pytest.mark.parametrize("form", [ep.EP_FORM_BF16, ep.EP_FORM_FP8, ep.EP_FORM_MXFP4])
+def test_products_on_their_operands(form):
+    width = {ep.EP_FORM_BF16: 2 * K, ep.EP_FORM_FP8: K, ep.EP_FORM_MXFP4: K // 2}[form]
+    arrays = dict(rows=ROWS * width, weights=E * N * width, out=ROWS * N * 2)
+    if form == ep.EP_FORM_FP8:
+        arrays.update(row_scales=ROWS * K // 128 * 4, weight_scales=E * K // 128 * 4)
+    elif form == ep.EP_FORM_MXFP4:
+        arrays.update(row_scales=ROWS * K // 32, weight_scales=E * N * K // 32)
+    for what, p in overlapping(arrays, ["out"]):
+        assert code_of(ep.ep_expert_gemm, groups(), form, p["rows"], p.get("row_scales"), p["weights"],
+                       p.get("weight_scales"), K, N, p["out"], 0) == ep.EP_ERR_ARG, what
+
+
+def test_gradients_on_their_operands():
+    for what, p in overlapping(dict(d=ROWS * N * 2, w=E * N * K * 2, out=ROWS * K * 2), ["out"]):
+        assert code_of(ep.ep_expert_gemm_dgrad, groups(), p["d"], p["w"], K, N, p["out"], 0) == ep.EP_ERR_ARG, what
+    for f32 in (False, True):
+        for what, p in overlapping(dict(d=ROWS * N * 2, x=ROWS * K * 2, out=E * N * K * (4 if f32 else 2)), ["out"]):
+            assert code_of(ep.ep_expert_gemm_wgrad, groups(), p["d"], p["x"], K, N, p["out"], f32, False,
+                           0) == ep.EP_ERR_ARG, what
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_row_operators_on_their_operands(grouped):
+    g = groups() if grouped else None
+    n = ROWS * K
+    for form, size, scales in ((ep.EP_FORM_BF16, 2 * n, 0), (ep.EP_FORM_FP8, n, n // 32), (ep.EP_FORM_MXFP4, n // 2, n // 32)):
+        arrays = dict(x=4 * n, out=size, **(dict(scales=scales) if scales else {}))
+        for what, p in overlapping(arrays, [a for a in arrays if a != "x"]):
+            assert code_of(ep.ep_swiglu, g, p["x"], ROWS, K, form, p["out"], p.get("scales"), 0) == ep.EP_ERR_ARG, what
+    for what, p in overlapping(dict(d=2 * n, x=4 * n, out=4 * n), ["out"]):
+        assert code_of(ep.ep_swiglu_backward, g, p["d"], p["x"], ROWS, K, p["out"], 0) == ep.EP_ERR_ARG, what
+    for what, p in overlapping(dict(x=2 * n, q=n // 2, scales=n // 32), ["q", "scales"]):
+        assert code_of(ep.ep_quantize_mxfp4, g, p["x"], ROWS, K, p["q"], p["scales"], 0) == ep.EP_ERR_ARG, what
+    for what, p in overlapping(dict(x=2 * n, q=n // 2, scales=n // 32), ["x"]):
+        assert code_of(ep.ep_dequantize_mxfp4, g, p["q"], p["scales"], ROWS, K, p["x"], 0) == ep.EP_ERR_ARG, what
+    # in place over an input that is another array's too
+    assert code_of(ep.ep_swiglu_backward, g, BASE, BASE, ROWS, K, BASE, 0) == ep.EP_ERR_ARG
