@@ -80,39 +80,38 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
 // compiler, which cannot tell the ring's buffers apart, otherwise waits for
 // all copies in flight before every LDS read; the instruction has no result
 // register, and the waits are wait_copies() below. M0 holds the LDS address
-// (the compiler keeps no value of its own there across: it is a clobber) and
-// needs one wait state before its use; a base that a vector instruction
+// and needs one wait state before its use; a base that a vector instruction
 // wrote needs five, which no place in the compiled kernels falls short of (a
 // test reads them).
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+                 : "memory");
 }
 // the same for bytes that nothing reads again: they take no other line's place in the caches
 __device__ __forceinline__ void copy16_once(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+                 : "memory");
 }
 // the same with an address per lane
 __device__ __forceinline__ void copy16(const uint8_t *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void copy4(const uint8_t *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+                 : "memory");
 }
 
 // Wait until at most `N` of this wave's copies are in flight and its LDS
