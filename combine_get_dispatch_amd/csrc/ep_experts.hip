@@ -275,7 +275,7 @@ __device__ __forceinline__ void copy_step(const P &p, uint32_t stage, int step, 
 template <class P>
 __device__ __forceinline__ void fill_ring(const P &p, uint32_t ring, int steps, int whole) {
     constexpr int S = P::kStages;
-    if (P::kRuns) p.first_run();
+    if constexpr (P::kRuns) p.first_run();
 #pragma unroll
     for (int i = 0; i < S; ++i)
         if (i < steps) copy_step(p, ring + i * P::kStage, i, whole, 0, i == S - 1 ? P::kSoon : P::kPer);
@@ -602,7 +602,7 @@ struct Product {
                     const bool ok = WTR ? step * 64 + (ins * 64 + lane) / (BN / 8) < K : in;
                     copy16(ok ? wb + step * wstep + wo[i] : zero, to);
                 }
-            } else if (RUNS) {  // this step's share of the next run
+            } else if constexpr (RUNS) {  // this step's share of the next run
                 copy_run(step / kRun + 1, step & 1);
             } else if (c < kXPer + kWPer + kXsPer) {
                 const int i = c - kXPer - kWPer;
@@ -892,7 +892,6 @@ struct Wgrad {
                         : base + (int64_t)step * 64 * width + off;
         copy16(p, to);
     }
-    __device__ __forceinline__ void first_run() const {}
     struct Half {
         uint32_t stage;
         int s;

@@ -1,6 +1,7 @@
 """What the experts' binding and C ABI refuse before anything is launched, in
 sizes and tensors that no GPU is needed for."""
 import os
+import subprocess
 
 import pytest
 import torch
@@ -135,3 +136,26 @@ def test_row_operators_on_their_operands(grouped):
         assert code_of(ep.ep_dequantize_mxfp4, g, p["q"], p["scales"], ROWS, K, p["x"], 0) == ep.EP_ERR_ARG, what
     # in place over an input that is another array's too
     assert code_of(ep.ep_swiglu_backward, g, BASE, BASE, ROWS, K, BASE, 0) == ep.EP_ERR_ARG
+
+
+# ---------------------------------------------------------------------------
+# the compiled kernels
+# ---------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def compiled(tmp_path_factory):
+    """(assembly, the compiler's messages) of the experts' kernels, device and host passes."""
+    out = str(tmp_path_factory.mktemp("experts") / "experts.s")
+    cmd = [epbuild.hipcc()] + epbuild.flags() + ["-S", "-o", out, os.path.join(epbuild.CSRC, "ep_experts.hip")]
+    done = subprocess.run(cmd + ["--offload-device-only"], check=True, capture_output=True, text=True)
+    host = subprocess.run([epbuild.hipcc()] + epbuild.flags() + ["--offload-host-only", "-fsyntax-only", cmd[-1]],
+                          check=True, capture_output=True, text=True)
+    return open(out).read(), done.stderr + host.stderr
+
+
+@pytest.mark.slow
+def test_no_warnings(compiled):
+    """But for the driver's own about flags that one of its passes does not use."""
+    found = [l for l in compiled[1].splitlines()
+             if "warning:" in l and "argument unused" not in l and "packed-fp32-ops" not in l]
+    assert not found, "\n".join(found[:5])
