@@ -80,9 +80,11 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
 // compiler, which cannot tell the ring's buffers apart, otherwise waits for
 // all copies in flight before every LDS read; the instruction has no result
 // register, and the waits are wait_copies() below. M0 holds the LDS address
-// and needs one wait state before its use; a base that a vector instruction
-// wrote needs five, which no place in the compiled kernels falls short of (a
-// test reads them).
+// and needs one wait state before its use. The compiler reserves M0 (its
+// register allocation never uses it, and it takes no clobber by that name);
+// no other instruction of the kernels writes or reads it. A base that a vector
+// instruction wrote needs five wait states. A test reads both in the compiled
+// kernels.
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
     base = uniform(base);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),

@@ -1,6 +1,7 @@
 """What the experts' binding and C ABI refuse before anything is launched, in
 sizes and tensors that no GPU is needed for."""
 import os
+import re
 import subprocess
 
 import pytest
@@ -159,3 +160,22 @@ def test_no_warnings(compiled):
     found = [l for l in compiled[1].splitlines()
              if "warning:" in l and "argument unused" not in l and "packed-fp32-ops" not in l]
     assert not found, "\n".join(found[:5])
+
+
+@pytest.mark.slow
+def test_only_the_copies_touch_m0(compiled):
+    """The copies to LDS write M0 in asm, which cannot be named as a clobber (the compiler reserves it): no instruction of
+    the compiler's own may write it, nor read it but as the copies do."""
+    in_asm, copies, others = False, 0, []
+    for line in compiled[0].splitlines():
+        t = line.strip()
+        if t.startswith(";;#ASM"):
+            in_asm = "START" in t
+        t = t.split(";")[0].strip()
+        if re.search(r"\bm0\b", t):
+            copies += in_asm
+            others += [] if in_asm else [t]
+        elif not in_asm:
+            # instructions that read it without naming it
+            others += [t] if re.match(r"(global|buffer)_load_lds|ds_gws|s_sendmsg\b|s_movrel|v_movrel|ds_\w+_addtid", t) else []
+    assert copies > 1000 and not others, others[:5]
