@@ -139,6 +139,83 @@ def test_row_operators_on_their_operands(grouped):
     assert code_of(ep.ep_swiglu_backward, g, BASE, BASE, ROWS, K, BASE, 0) == ep.EP_ERR_ARG
 
 
+# Tensors wrong in one respect. (The names of the arguments, in the order of the call; `out` last, a tuple of them where the
+# call has two outputs.)
+def binding_calls():
+    i32, bf, u8, f32 = torch.int32, torch.bfloat16, torch.uint8, torch.float32
+    t = lambda dtype, *shape: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    E, R, cap, K, N = 4, 2, 8, 256, 136
+    n = R * cap
+    g = dict(counts=t(i32, E), offsets=t(i32, E))
+    gemm = {
+        "bf16": dict(rows=t(bf, n, K), weights=t(bf, E, N, K)),
+        "fp8": dict(rows=t(u8, n, K), weights=t(u8, E, N, K), row_scales=t(f32, n, 2), weight_scales=t(f32, E, 2, 2)),
+        "mxfp4": dict(rows=t(u8, n, K // 2), weights=t(u8, E, N, K // 2), row_scales=t(u8, n, 8),
+                      weight_scales=t(u8, E, N, 8)),
+    }
+    mk = lambda d: ep.Groups(d.pop("counts"), d.pop("offsets"), num_experts=E, num_ranks=R, cap_rows=cap)  # noqa: E731
+    calls = {f"expert_gemm {f}": (lambda d: ep.expert_gemm(groups=mk(d), **d), dict(g, **a, out=t(bf, n, N)))
+             for f, a in gemm.items()}
+    calls["expert_gemm_dgrad"] = (lambda d: ep.expert_gemm_dgrad(groups=mk(d), **d),
+                                  dict(g, grad_out=t(bf, n, N), weights=t(bf, E, N, K), out=t(bf, n, K)))
+    calls["expert_gemm_wgrad"] = (lambda d: ep.expert_gemm_wgrad(groups=mk(d), dtype=f32, **d),
+                                  dict(g, grad_out=t(bf, n, N), rows=t(bf, n, K), out=t(f32, E, N, K)))
+    pair = lambda d: (d.pop("out"), d.pop("scales"))  # noqa: E731
+    calls["swiglu bf16"] = lambda d: ep.swiglu(groups=mk(d), **d), dict(g, gate_up=t(bf, n, 2 * K), out=t(bf, n, K))
+    calls["swiglu fp8"] = (lambda d: ep.swiglu(d.pop("gate_up"), mk(d), "fp8", out=pair(d)),
+                           dict(g, gate_up=t(bf, n, 2 * K), out=t(u8, n, K), scales=t(f32, n, 2)))
+    calls["swiglu mxfp4"] = (lambda d: ep.swiglu(d.pop("gate_up"), mk(d), "mxfp4", out=pair(d)),
+                             dict(g, gate_up=t(bf, n, 2 * K), out=t(u8, n, K // 2), scales=t(u8, n, 8)))
+    calls["swiglu_backward"] = (lambda d: ep.swiglu_backward(groups=mk(d), **d),
+                                dict(g, grad_out=t(bf, n, K), gate_up=t(bf, n, 2 * K), out=t(bf, n, 2 * K)))
+    calls["quantize_mxfp4"] = (lambda d: ep.quantize_mxfp4(d.pop("x"), mk(d), out=pair(d)),
+                               dict(g, x=t(bf, n, K), out=t(u8, n, K // 2), scales=t(u8, n, 8)))
+    calls["dequantize_mxfp4"] = (lambda d: ep.dequantize_mxfp4(d.pop("q"), d.pop("scales"), mk(d), **d),
+                                 dict(g, q=t(u8, n, K // 2), scales=t(u8, n, 8), out=t(bf, n, K)))
+    return calls
+
+
+def wrong(t):
+    """The tensor with another type of the same size, another size, and other strides."""
+    same_size = {torch.int32: torch.float32, torch.float32: torch.int32, torch.bfloat16: torch.float16,
+                 torch.uint8: torch.int8}
+    yield "type", t.view(same_size[t.dtype])
+    yield "dimensions", t[None]
+    for d in range(t.dim()):
+        yield f"size {d}", torch.zeros([s + 32 if i == d else s for i, s in enumerate(t.shape)], dtype=t.dtype)
+    if t.dim() > 1:
+        yield "order", t.mT.contiguous().mT
+    yield "stride", torch.zeros([2 * s if i == 0 else s for i, s in enumerate(t.shape)], dtype=t.dtype)[::2]
+
+
+@pytest.mark.parametrize("name", list(binding_calls()))
+def test_binding_refuses_each_tensor(as_if_on_gpu, name):
+    call, tensors = binding_calls()[name]
+    call(dict(tensors))
+    assert [c for c, _ in as_if_on_gpu] == ["ep_" + name.split()[0]]  # as it should be: it reaches the C call, once
+    as_if_on_gpu.clear()
+    for arg, t in tensors.items():
+        for what, bad in wrong(t):
+            try:
+                call(dict(tensors, **{arg: bad}))
+            except ep.EpError as e:
+                assert e.code == ep.EP_ERR_ARG
+            assert not as_if_on_gpu, f"{arg} of wrong {what}"
+
+
+def test_binding_refuses_other_devices(monkeypatch):
+    """Every tensor is another device's in turn."""
+    monkeypatch.setattr(ep, "_torch", torch)
+    monkeypatch.setattr(ep, "_device", lambda: 0)
+    monkeypatch.setattr(ep, "_raw_stream", lambda dev: 0)
+    for name, (call, tensors) in binding_calls().items():
+        for arg in tensors:
+            places = {t.data_ptr(): 0 for t in tensors.values()}
+            places[tensors[arg].data_ptr()] = 1
+            monkeypatch.setattr(torch.Tensor, "get_device", lambda t: places[t.data_ptr()])
+            assert code_of(call, dict(tensors)) == ep.EP_ERR_ARG, (name, arg)
+
+
 # ---------------------------------------------------------------------------
 # the compiled kernels
 # ---------------------------------------------------------------------------
