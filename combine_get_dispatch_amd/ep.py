@@ -317,56 +317,63 @@ def _ref(groups: Optional[EpGroups]):
     return None if groups is None else ctypes.byref(groups)
 
 
-def _c_ints(*sizes: int) -> None:
-    """Refuse sizes that a C int cannot hold (ctypes would pass their low 32 bits)."""
-    for n in sizes:
-        if not -1 << 31 <= n < 1 << 31:
-            raise EpError(EP_ERR_ARG, f"{n} does not fit 32 bits")
+def _not_c_ints(*sizes: int) -> None:
+    """Refuse sizes that a C int cannot hold, of which ctypes would pass the low
+    32 bits, and negative ones. (Callers test by shifts: a call each took 0.4 us
+    of a short product's 8.)"""
+    raise EpError(EP_ERR_ARG, f"{sizes}: not sizes of 31 bits")
 
 
 def ep_expert_gemm(groups: EpGroups, form: int, rows: int, row_scales: Optional[int], weights: int,
                    weight_scales: Optional[int], K: int, N: int, out: int, stream: int) -> None:
-    _c_ints(K, N)
+    if (K | N) >> 31:
+        _not_c_ints(K, N)
     _check(load().ep_expert_gemm(_ref(groups), form, rows, row_scales, weights, weight_scales, K, N, out, stream),
            "ep_expert_gemm")
 
 
 def ep_expert_gemm_dgrad(groups: EpGroups, grad_out: int, weights: int, K: int, N: int, grad_rows: int,
                          stream: int) -> None:
-    _c_ints(K, N)
+    if (K | N) >> 31:
+        _not_c_ints(K, N)
     _check(load().ep_expert_gemm_dgrad(_ref(groups), grad_out, weights, K, N, grad_rows, stream),
            "ep_expert_gemm_dgrad")
 
 
 def ep_expert_gemm_wgrad(groups: EpGroups, grad_out: int, rows: int, K: int, N: int, grad_weights: int, out_f32: bool,
                          accumulate: bool, stream: int) -> None:
-    _c_ints(K, N)
+    if (K | N) >> 31:
+        _not_c_ints(K, N)
     _check(load().ep_expert_gemm_wgrad(_ref(groups), grad_out, rows, K, N, grad_weights, int(out_f32), int(accumulate),
                                        stream), "ep_expert_gemm_wgrad")
 
 
 def ep_swiglu(groups: Optional[EpGroups], gate_up: int, num_rows: int, I: int, form: int, out: int,
               scales: Optional[int], stream: int) -> None:
-    _c_ints(I)
+    if I >> 31:
+        _not_c_ints(I)
     _check(load().ep_swiglu(_ref(groups), gate_up, num_rows, I, form, out, scales, stream), "ep_swiglu")
 
 
 def ep_swiglu_backward(groups: Optional[EpGroups], grad_out: int, gate_up: int, num_rows: int, I: int,
                        grad_gate_up: int, stream: int) -> None:
-    _c_ints(I)
+    if I >> 31:
+        _not_c_ints(I)
     _check(load().ep_swiglu_backward(_ref(groups), grad_out, gate_up, num_rows, I, grad_gate_up, stream),
            "ep_swiglu_backward")
 
 
 def ep_quantize_mxfp4(groups: Optional[EpGroups], x: int, num_rows: int, cols: int, q: int, scales: int,
                       stream: int) -> None:
-    _c_ints(cols)
+    if cols >> 31:
+        _not_c_ints(cols)
     _check(load().ep_quantize_mxfp4(_ref(groups), x, num_rows, cols, q, scales, stream), "ep_quantize_mxfp4")
 
 
 def ep_dequantize_mxfp4(groups: Optional[EpGroups], q: int, scales: int, num_rows: int, cols: int, x: int,
                         stream: int) -> None:
-    _c_ints(cols)
+    if cols >> 31:
+        _not_c_ints(cols)
     _check(load().ep_dequantize_mxfp4(_ref(groups), q, scales, num_rows, cols, x, stream), "ep_dequantize_mxfp4")
 
 
@@ -726,7 +733,8 @@ class Groups:
         shape = (self.num_experts, self.num_ranks) if self.region_rows else (self.num_experts,)
         counts = _tensor(self.counts, "counts", _torch.int32, shape, dev)
         offsets = None if self.offsets is None else _tensor(self.offsets, "offsets", _torch.int32, shape, dev)
-        _c_ints(self.num_experts, self.num_ranks)
+        if (self.num_experts | self.num_ranks) >> 31:
+            _not_c_ints(self.num_experts, self.num_ranks)
         return EpGroups(offsets, counts, self.num_experts, self.num_ranks, self.cap_rows, self.region_rows,
                         self.rows_hint)
 
