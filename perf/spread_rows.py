@@ -5,8 +5,9 @@ that every token takes the same k experts: T rows each, the others none.)
 
     python3 perf/spread_rows.py [case ...]
 
-For each case: the time of a pass (HIP events around 20 passes back to back,
-alternating between two sets of inputs; the median of five such runs), the
+For each case: the time of a pass (HIP events around 50 ms of passes back to
+back, 20 at least, alternating between two sets of inputs; the median of five
+such runs, after one that is not counted), the
 bytes and operations of `work` over it, and how far the result is from the
 64-bit form (root mean square over root mean square).
 """
@@ -46,20 +47,23 @@ def routing(case, g):
                 cap=int(per_rank.sum(1).max()) + 3, region=0, widest=int(counts.max()))
 
 
-def timed(states, passes=20, runs=5):
-    for s in states:
-        operators.run(s)
-    times = []
-    for _ in range(runs):
-        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-        torch.cuda.synchronize()
-        start.record()
-        for i in range(passes):
-            operators.run(states[i % len(states)])
-        end.record()
-        torch.cuda.synchronize()
-        times.append(start.elapsed_time(end) * 1e-3 / passes)
-    return sorted(times)[runs // 2]
+def burst(states, passes):
+    """Seconds a pass, of so many back to back."""
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    start.record()
+    for i in range(passes):
+        operators.run(states[i % len(states)])
+    end.record()
+    torch.cuda.synchronize()
+    return start.elapsed_time(end) * 1e-3 / passes
+
+
+def timed(states, runs=5):
+    burst(states, 2 * len(states))
+    passes = max(20, int(0.05 / burst(states, 4)))
+    burst(states, passes)  # the clocks settle
+    return sorted(burst(states, passes) for _ in range(runs))[runs // 2]
 
 
 def distance(got, want):
