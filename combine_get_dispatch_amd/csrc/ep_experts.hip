@@ -17,12 +17,14 @@
 // (FP8, whose sums pass through vector registers to be scaled: eight waves of
 // 128 x 64). 128 x 128, two workgroups per CU, where an expert has few rows
 // and the weights' bytes are the time. On MI355X: gradients of 32768 rows, 8
-// experts of 4096 x 7168: 1.28 PFLOP/s (a library product of that size 1.52);
-// FP8, 32768 rows on 8 experts of the same size: 2.27 PFLOP/s (2.94); MXFP4,
-// 16384 rows: 3.8 PFLOP/s; 1024 rows on 256 experts, 7.4 GB of FP8 weights:
-// 1090 us, 6.8 TB/s. What bounds the large ones: bf16 the clock under matrix
-// instructions; FP8 the issue of one scale addition per result and 128
-// channels; MXFP4 the ring's filling and the results' writes around 28 steps.
+// experts of 4096 x 7168: 1.27 PFLOP/s (a library product of that size 1.52);
+// FP8, 32768 rows on 8 experts of the same size: 2.25 PFLOP/s (2.94), on 64,
+// ragged, 1.76; MXFP4, 16384 rows: 3.8 PFLOP/s; 1024 rows on 256 experts, 7.4 GB
+// of FP8 weights: 1090 us, 6.8 TB/s. What bounds the large ones: bf16 the clock
+// under matrix instructions; FP8 no one thing (the matrix unit works 57% of the
+// time, beside it 148 vector instructions a step and wave, most of them scale
+// additions); MXFP4 the ring's filling and the results' writes around 28 steps,
+// and LDS bank conflicts (17% of the cycles).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -733,7 +735,12 @@ struct Product {
     // Tile height: the counts are known here only. The fewest rounds of the
     // grid, each as long as its tiles are high (and some 96 rows' time more,
     // for what a tile costs whatever its height): a batch whose rows are few,
-    // or all on one expert, gets lower tiles on more compute units.
+    // or all on one expert, gets lower tiles on more compute units. Without the
+    // 96 rows' time 32768 ragged FP8 rows on 64 experts take 1502 us in place
+    // of 1096, 16384 MXFP4 rows on 8 experts 461 in place of 298 (with 300 rows'
+    // time as with 96). Always at the full height 128 FP8 rows on each of 8
+    // experts take 96 us in place of 81, 256 MXFP4 rows on one 41 in place of
+    // 27. (That lower tiles read the weights again is not counted.)
     static __device__ __forceinline__ int choose_height(const ProductArgs &a, Shared &sh, int ntiles) {
         const int tid = threadIdx.x;
         if (tid < 3) sh.tiles[tid] = 0;
@@ -1114,8 +1121,9 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     a.out_f32 = out_f32 != 0;
     a.accumulate = accumulate != 0;
     // 256 x 256 tiles where there are enough for the chip and rows enough to sum, else 128 x 128 (48 experts of 7 rows,
-    // 126 MB of fp32 results: 27.5 us against 58; 8 experts of 4096 rows, 4096 x 7168: 1.5 ms against 2.4), and the
-    // looked-up rows of the low-latency layout, whose wide tile has no registers for the look-up
+    // 126 MB of fp32 results: 27.5 us against 58; 8 experts of 4096 rows, 4096 x 7168: 1.5 ms against 2.4). The low-latency
+    // layout takes the small tile: its rows are looked up for each copy, which keeps the loop from being unrolled and puts
+    // the accumulators into scratch memory (2048 rows on 64 experts of 4096 x 2048: 3.1 ms against 0.6 for packed rows)
     const int64_t big = (int64_t)a.g.E * ((N + 255) / 256) * ((K + 255) / 256);
     const bool wide = big >= cus && ep::group_rows_expected(groups) >= 128 * (int64_t)a.g.E;
     const hipStream_t s = (hipStream_t)stream;

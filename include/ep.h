@@ -496,6 +496,8 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
 /* SwiGLU between the experts' two products: h[p][i] = silu(gate) * up with
  * gate = gate_up[p][i], up = gate_up[p][I + i], silu(g) = g / (1 + exp(-g)),
  * in fp32, for every row p that an expert has (groups NULL: all num_rows rows).
+ * (1 / (1 + exp(-g)) below 2^-126, for g below -87.3, may be taken as 0, here
+ * and in the gradient.)
  * gate_up: [num_rows][2*I] bf16; num_rows = R*cap_rows where groups are given.
  *   EP_FORM_BF16: out [num_rows][I] bf16; scales NULL.
  *   EP_FORM_FP8: out bytes [num_rows][I], scales fp32 [num_rows][I/128], by the
