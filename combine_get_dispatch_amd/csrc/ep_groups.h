@@ -32,11 +32,11 @@ int64_t group_rows_expected(const ep_groups *g);
 int device_cus(int *cus);
 int hip_status(hipError_t e, const char *what);
 
-// Host side: whether two arrays share bytes (NULL shares none). Workgroups
+// Host side: whether two arrays share bytes (NULL and empty ones none). Workgroups
 // write results while others still read operands, so no output may.
 inline bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
 }
 
 __device__ __forceinline__ int group_region_count(const GroupArgs &g, int e, int s) {

@@ -3,11 +3,11 @@
 //
 // All four read every value once and write every value once: they are bound
 // by memory, SwiGLU to FP8 by its vector instructions (the SIMDs issue them in
-// 97% of their cycles). A wave takes chunks of 512 channels of a row, 8 a lane (16 bytes
-// of bf16, neighbouring lanes neighbouring addresses: 32 channels a lane, a
-// whole scale group, took 2.3 times as long to write), a run of neighbouring
-// chunks per wave, kUnroll chunks' loads in flight together. A scale group of
-// 32 channels is four lanes, one of 128 sixteen.
+// 97% of their cycles). A wave takes chunks of 512 channels of a row, 8 a lane
+// (16 bytes of bf16, neighbouring lanes neighbouring addresses: 32 channels a
+// lane, a whole scale group, took 2.3 times as long to write), a run of
+// neighbouring chunks per wave, kUnroll chunks' loads in flight together. A
+// scale group of 32 channels is four lanes, one of 128 sixteen.
 //
 // On MI355X: SwiGLU of 32768 rows x 2048 to bf16 68 us (403 MB, 5.95 TB/s), to
 // FP8 72 us (338 MB, 4.7 TB/s), its gradient on 65536 rows 236 us (1.34 GB, 5.7

@@ -59,3 +59,13 @@ def test_adjacent_arrays(order):
     same(lambda i, o: ep.quantize_mxfp4(i[0], g, out=o), [x], [zeros(cap, K // 2, dtype=u8), zeros(cap, 8, dtype=u8)])
     q, s = xh.make_operand(rng, (cap, K), "mxfp4")
     same(lambda i, o: ep.dequantize_mxfp4(*i, g, out=o[0]), [q, s], [zeros(cap, K)])
+
+
+def test_empty_rows_share_no_memory():
+    """No receive rows: the weight gradients are zeros, whatever the row arrays' pointers are."""
+    counts = torch.zeros(4, dtype=torch.int32).cuda()
+    g = ep.Groups(counts, counts, num_experts=4, num_ranks=2, cap_rows=0).c()
+    out = torch.full((4, 24, 40), 7.0, device="cuda")
+    inside = out.data_ptr() + 64
+    ep.ep_expert_gemm_wgrad(g, inside, inside, 40, 24, out.data_ptr(), True, False, torch.cuda.current_stream().cuda_stream)
+    assert bool((out == 0).all())
