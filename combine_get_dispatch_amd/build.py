@@ -27,7 +27,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libep.so")
 SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_api.hip"), os.path.join(CSRC, "ep_patterns.hip"),
-           os.path.join(CSRC, "ep_experts.hip"), os.path.join(CSRC, "ep_rows.hip")]
+           os.path.join(CSRC, "ep_experts.hip"), os.path.join(CSRC, "ep_rows.hip"), os.path.join(CSRC, "ep_router.hip")]
 HEADERS = [os.path.join(CSRC, "ep_internal.h"), os.path.join(CSRC, "ep_groups.h"), os.path.join(INCLUDE, "ep.h")]
 ARCH = "gfx950"
 

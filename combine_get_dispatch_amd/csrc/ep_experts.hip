@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "ep.h"
 #include "ep_groups.h"
@@ -48,7 +49,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // read through the scalar cache: the kernels never write it
 typedef const __attribute__((address_space(4))) float *constant_f32;
 
-enum Form { kBf16 = EP_FORM_BF16, kFp8 = EP_FORM_FP8, kMx4 = EP_FORM_MXFP4 };
+enum Form { kBf16 = EP_FORM_BF16, kFp8 = EP_FORM_FP8, kMx4 = EP_FORM_MXFP4, kInt8 = EP_FORM_INT8 };
 
 constexpr int kStepBytes = 128;  // of a row, per reduction step
 
@@ -59,8 +60,8 @@ struct ProductArgs {
     GroupArgs g;
     const uint8_t *x;        // rows, x_bytes each
     const uint8_t *w;        // [E][w_rows][w_bytes]
-    const uint8_t *x_scales; // FP8: fp32 [rows][K/128]; MX4: bytes [rows][K/32]
-    const uint8_t *w_scales; // FP8: fp32 [E][ceil(N/128)][K/128]; MX4: bytes [E][N][K/32]
+    const uint8_t *x_scales; // FP8: fp32 [rows][K/128]; MX4: bytes [rows][K/32]; INT8: fp32 [rows]
+    const uint8_t *w_scales; // FP8: fp32 [E][ceil(N/128)][K/128]; MX4: bytes [E][N][K/32]; INT8: fp32 [E][N]
     uint16_t *out;           // [rows][N] bf16
     int K, N;                // reduction length and output channels
     int steps;               // reduction steps
@@ -235,6 +236,15 @@ __device__ __forceinline__ void mfma_bf16(i32x4 a, i32x4 b, f32x4 &c) {
                                                     0, 0);
 }
 
+// the same of 8-bit integers: c holds 32-bit integers
+template <bool ACC>
+__device__ __forceinline__ void mfma_int8(i32x4 a, i32x4 b, f32x4 &c) {
+    if constexpr (ACC)
+        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : EP_ACC(c) : "v"(a), "v"(b));
+    else
+        c = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(i32x4, c), 0, 0, 0));
+}
+
 // as: the scale byte of the lane's 32 values of a, in the word's low byte
 template <bool ACC>
 __device__ __forceinline__ void mfma_mx4(i32x4 a, i32x4 b, f32x4 &c, int as, int bs) {
@@ -346,6 +356,83 @@ __device__ __forceinline__ void reduce(const P &p, uint32_t ring, int steps, int
     while (step + S < whole) body(std::integral_constant<int, kWhole>());
     if (!P::kRuns)
         while (step + S < steps) body(std::integral_constant<int, kPartial>());
+    while (step < steps) body(std::integral_constant<int, kLast>());
+}
+
+template <class F, int... I>
+__device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// The reduction of a weight gradient whose rows' side is kept in 8 bits: as
+// above, with two buffers, but for that side, which a copy to LDS cannot widen.
+// Its codes are loaded to registers when a buffer has been read out (fetch),
+// widened and written to LDS in the next step's first half, a word of four
+// between four matrix instructions (put), and read from the step's middle on.
+// (The compiler waits for these loads by itself; it counts no copies to LDS, and
+// so waits for no less than it has to.)
+template <class P>
+__device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
+    constexpr int ACT = P::ACT, NT = P::NT;
+    static_assert(P::kStages == 2, "two buffers");
+    const uint32_t other = ring + P::kStage;
+    if constexpr (P::kTable) {
+        p.look_up(0);
+        p.look_up(1);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    if (0 < whole) p.template fetch<true>(0); else p.template fetch<false>(0);
+    copy_step(p, ring, 0, whole, 0, P::kPer);
+#pragma unroll
+    for (int w = 0; w < P::kWords; ++w) p.put(ring, w);
+    if (1 < steps) {
+        if (1 < whole) p.template fetch<true>(1); else p.template fetch<false>(1);
+        copy_step(p, other, 1, whole, 0, P::kPer);
+    }
+    wait_copies<0>();
+    typename P::Frags h0, h1;
+#pragma unroll
+    for (int f = 0; f < P::kReads; ++f) p.read(h0, p.place(ring, 0, 0), f);
+    int step = 0;
+    uint32_t st = ring, nx = other;
+    auto body = [&](auto copies) __attribute__((always_inline)) {
+        constexpr int COPIES = decltype(copies)::value;
+        constexpr int M = ACT * NT, R = P::kReads, C = P::kPer, H = M / (2 * C), W = P::kWords;
+        const auto half = p.place(st, step, 1), next = p.place(nx, step + 1, 0);
+        if (P::kTable && COPIES != kLast) p.look_up(step + 2);
+        const bool more = COPIES != kLast || step + 1 < steps;
+        each([&](auto at) __attribute__((always_inline)) {  // (as a loop it is too much for the compiler to unroll)
+            constexpr int m = decltype(at)::value;
+#pragma unroll
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h1, half, f);
+            p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
+            if (more) {
+#pragma unroll
+                for (int w = m * W / M; w < (m + 1) * W / M; ++w) p.put(nx, w);
+            }
+            if (m % 2) pin();
+        }, std::make_integer_sequence<int, M>());
+        wait_copies<0>();
+        if (COPIES != kLast) p.template fetch<COPIES == kWhole>(step + 2);
+        pin();
+        each([&](auto at) __attribute__((always_inline)) {
+            constexpr int m = decltype(at)::value;
+#pragma unroll
+            for (int f = (m + H) * C / M; f < (m + 1 + H) * C / M && f < C; ++f)  // between the reads
+                if (COPIES != kLast) p.template copy<COPIES == kWhole>(step + 2, st, f);
+#pragma unroll
+            for (int f = m * R / M; f < (m + 1) * R / M; ++f) p.read(h0, next, f);
+            p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
+            if (m % 2) pin();
+        }, std::make_integer_sequence<int, M>());
+        if (P::kAcc && COPIES == kLast) settle();
+        const uint32_t t = st;
+        st = nx;
+        nx = t;
+        ++step;
+    };
+    while (step + 2 < whole) body(std::integral_constant<int, kWhole>());
+    while (step + 2 < steps) body(std::integral_constant<int, kPartial>());
     while (step < steps) body(std::integral_constant<int, kLast>());
 }
 
@@ -463,7 +550,7 @@ struct Product {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int MOST = 16 * WM * MT, NTILES = BN / 16 / WN;
     static constexpr bool kAccumulate = MT * NTILES >= 64;  // 256 accumulators a lane: all registers of a SIMD
-    static constexpr bool kScaled = FORM != kBf16;
+    static constexpr bool kScaled = FORM == kFp8 || FORM == kMx4;  // along the reduction
     // steps per run of scales, and the runs' bytes (three in LDS: one read, one or two on their way)
     static constexpr int kRun = FORM == kFp8 ? 4 : 2, kXsRun = RUNS ? MOST * 16 : 0;
     static constexpr int kWsRun = RUNS && FORM == kMx4 ? BN * 16 : 0;
@@ -520,7 +607,7 @@ struct Product {
             : wave(wave_), lane(lane_), K(a.K) {
             scales = lds_address(sh.scales);
             const int64_t row0 = __builtin_amdgcn_readfirstlane(sh.row[0]);
-            row_bytes = FORM == kBf16 ? a.K * 2 : FORM == kFp8 ? a.K : a.K / 2;
+            row_bytes = FORM == kBf16 ? a.K * 2 : FORM == kMx4 ? a.K / 2 : a.K;
             xb = uniform(a.x + row0 * row_bytes);
             const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
@@ -694,6 +781,8 @@ struct Product {
         __device__ __forceinline__ void mfma(const Frags &h, int i, int j, f32x4 &c) const {
             if constexpr (FORM == kMx4)
                 mfma_mx4<kAcc>(h.w[j], h.x[i], c, h.ws[j], h.xs[i]);
+            else if constexpr (FORM == kInt8)
+                mfma_int8<kAcc>(h.w[j], h.x[i], c);
             else
                 mfma_bf16<kAcc>(h.w[j], h.x[i], c);
         }
@@ -717,10 +806,28 @@ struct Product {
         } else {
             reduce(t, ring, a.steps, t.row_bytes / kStepBytes, acc);
         }
+        // 8-bit integers: a lane's four channels of a column tile have four scales (past the last channel: any)
+        f32x4 ws[FORM == kInt8 ? NTILES : 1];
+        if constexpr (FORM == kInt8) {
+#pragma unroll
+            for (int j = 0; j < NTILES; ++j)
+                ws[j] = *(const f32x4 *)((const float *)a.w_scales + (int64_t)e * a.N +
+                                         min(n0 + (wn * NTILES + j) * 16 + (lane >> 4) * 4, a.N - 4));
+        }
 #pragma unroll
         for (int i = 0; i < ACT; ++i) {
             const int m = (wm + i * WM) * 16 + (lane & 15);
-            uint16_t *o = a.out + (int64_t)sh.row[m < rows ? m : 0] * a.N;
+            const int64_t row = sh.row[m < rows ? m : 0];
+            uint16_t *o = a.out + row * a.N;
+            if constexpr (FORM == kInt8) {
+                const float xs = ((const float *)a.x_scales)[row];
+#pragma unroll
+                for (int j = 0; j < NTILES; ++j) {
+                    const i32x4 sum = __builtin_bit_cast(i32x4, acc[i][j]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i][j][q] = (float)sum[q] * (xs * ws[j][q]);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < NTILES; j += 4) {
                 u32x4 v[2];
@@ -829,7 +936,8 @@ __global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_product(Prod
 
 struct WgradArgs {
     GroupArgs g;
-    const uint8_t *x;     // rows [..][K] bf16
+    const uint8_t *x;     // rows [..][K] bf16; kept ones: MXINT8 codes
+    const uint8_t *x_scales; // kept rows: bytes [..][K/32]
     const uint8_t *grad;  // rows [..][N] bf16
     void *out;            // [E][N][K] fp32 or bf16
     int K, N;
@@ -841,32 +949,55 @@ struct WgradArgs {
 // rows past the expert's last are zeros on both sides, so that whatever the
 // unused receive rows hold (NaN included) does not enter a sum. REGIONS: the
 // low-latency layout, whose rows are looked up one by one.
-template <int BM, int BN, int WM, int WN, bool REGIONS>
+//
+// KEPT: rows in MXINT8. They stand for bf16 numbers, so that widened (a whole
+// number times a power of two, exact) they give the same sums as those. A lane
+// widens 16 codes of a row, half a scale's group, at a time: 32 bytes of the
+// tile. Rows of regions are looked up once a step, into LDS.
+template <bool KEPT, int CHUNKS>
+struct KeptRows {};
+// the scales, a lane's places in them and in the tile, what it has loaded and widened, the looked-up rows' place in LDS
+template <int CHUNKS>
+struct KeptRows<true, CHUNKS> {
+    const uint8_t *sb;
+    uint32_t so[CHUNKS], to[CHUNKS], table;
+    u32x4 codes[CHUNKS], wide;
+    uint8_t scale[CHUNKS];
+};
+template <int BM, int BN, int WM, int WN, bool REGIONS, bool KEPT>
 struct Wgrad {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int ACT = BM / 16 / WM, NT = BN / 16 / WN;
     static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes, kStages = 2;
-    static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + kXPer;
+    static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + (KEPT ? 0 : kXPer);
     static constexpr int kSoon = kPer;
+    static constexpr int kChunks = kXBytes / 32 / kThreads, kWords = kChunks * 4;  // of 16 codes, and of 4, a lane's
+    static constexpr bool kTable = KEPT && REGIONS;
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
     using Frags = HalfFrags<ACT, NT, false>;
     static constexpr int kReads = ACT + NT;
     static constexpr bool kAcc = ACT * NT >= 64, kRuns = false;
 
-    struct Shared {
+    struct Plain {
         uint8_t ring[kStages * kStage];
     };
+    struct Table {
+        uint8_t ring[kStages * kStage];
+        int rows[128];  // receive rows of two steps
+    };
+    using Shared = std::conditional_t<kTable, Table, Plain>;
 
     const GroupArgs *g;
     const uint8_t *gb, *xb;  // bases: packed layout, the expert's first row; low-latency, the arrays
-    uint32_t go[kGPer], xo[kXPer];
+    uint32_t go[kGPer], xo[KEPT ? kChunks : kXPer];
     int e, count, wave, lane, grow, xrow;  // rows' bytes
+    KeptRows<KEPT, kChunks> kept;
 
     __device__ __forceinline__ Wgrad(const WgradArgs &a, int e_, int count_, int n0, int k0, int wave_, int lane_)
-        : g(&a.g), e(e_), count(count_), wave(wave_), lane(lane_), grow(a.N * 2), xrow(a.K * 2) {
+        : g(&a.g), e(e_), count(count_), wave(wave_), lane(lane_), grow(a.N * 2), xrow(a.K * (KEPT ? 1 : 2)) {
         const int64_t base = REGIONS || count == 0 ? 0 : ep::group_row(a.g, e, 0);
         gb = uniform(a.grad + base * grow + n0 * 2);
-        xb = uniform(a.x + base * xrow + k0 * 2);
+        xb = uniform(a.x + base * xrow + k0 * (KEPT ? 1 : 2));
         // columns past the end repeat the last chunk
 #pragma unroll
         for (int i = 0; i < kGPer; ++i) {
@@ -874,12 +1005,64 @@ struct Wgrad {
             tr_place<BM>(wave + i * kWaves, lane, r, c);
             go[i] = (uint32_t)r * grow + min(c, a.N - 8 - n0) * 2;
         }
+        if constexpr (KEPT) {
+            kept.sb = uniform(a.x_scales + base * (a.K / 32) + k0 / 32);
 #pragma unroll
-        for (int i = 0; i < kXPer; ++i) {
-            int r, c;
-            tr_place<BN>(wave + i * kWaves, lane, r, c);
-            xo[i] = (uint32_t)r * xrow + min(c, a.K - 8 - k0) * 2;
+            for (int i = 0; i < kChunks; ++i) {
+                const int at = i * kThreads + wave * 64 + lane, r = at / (BN / 16), u = at % (BN / 16);
+                const int c = min(u * 16, a.K - 16 - k0);
+                xo[i] = (REGIONS ? 0 : (uint32_t)r * xrow) + c;
+                kept.so[i] = (REGIONS ? 0 : (uint32_t)r * (xrow / 32)) + c / 32;
+                kept.to[i] = kGBytes + r * (BN * 2) + ((u ^ tr_swizzle(r)) << 5);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kXPer; ++i) {
+                int r, c;
+                tr_place<BN>(wave + i * kWaves, lane, r, c);
+                xo[i] = (uint32_t)r * xrow + min(c, a.K - 8 - k0) * 2;
+            }
         }
+    }
+
+    // Kept rows: rows of step `step` to LDS (of steps past the last: any).
+    __device__ __forceinline__ void look_up(int step) {
+        if (wave == 0) {
+            const int m = step * 64 + lane;
+            const int row = m < count ? (int)ep::group_row(*g, e, m) : 0;
+            *(__attribute__((address_space(3))) int *)(uintptr_t)(kept.table + ((step & 1) * 64 + lane) * 4) = row;
+        }
+    }
+    __device__ __forceinline__ int64_t looked_up(int step, int r) const {
+        return lds_read<int>(kept.table + ((step & 1) * 64 + r) * 4);
+    }
+
+    // Load a step's codes and scales; WHOLE: all 64 rows are the expert's (others: zeros).
+    template <bool WHOLE>
+    __device__ __forceinline__ void fetch(int step) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int r = (i * kThreads + wave * 64 + lane) / (BN / 16);
+            int64_t row = (int64_t)step * 64;
+            if constexpr (REGIONS) row = looked_up(step, r);
+            const uint8_t *q = xb + row * xrow + xo[i], *s = kept.sb + row * (xrow / 32) + kept.so[i];
+            if (!WHOLE && step * 64 + r >= count) q = s = (const uint8_t *)&k_zero_chunk;
+            kept.codes[i] = *(const u32x4 *)q;
+            kept.scale[i] = *s;
+        }
+    }
+    // Widen word w of the lane's codes, and write eight of them when they are done.
+    __device__ __forceinline__ void put(uint32_t stage, int w) {
+        const int i = w / 4;
+        const uint32_t word = kept.codes[i][w % 4], b = kept.scale[i];
+        const float unit = b == 255 ? __builtin_nanf("") : __uint_as_float(b > 6 ? (b - 6) << 23 : 1u << (16 + b));  // 2^(b-133)
+        uint32_t f[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] = __float_as_uint((float)((int)(word << (24 - 8 * c)) >> 24) * unit);
+        kept.wide[w % 2 * 2] = (f[1] & 0xFFFF0000u) | f[0] >> 16;
+        kept.wide[w % 2 * 2 + 1] = (f[3] & 0xFFFF0000u) | f[2] >> 16;
+        if (w % 2)
+            *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(stage + kept.to[i] + w % 4 / 2 * 16) = kept.wide;
     }
 
     template <bool WHOLE>
@@ -896,9 +1079,14 @@ struct Wgrad {
         }
         const int r = (ins * 64 + lane) / ((of_grad ? BM : BN) / 8), m = step * 64 + r;
         const uint8_t *p = (const uint8_t *)&k_zero_chunk;
-        if (m < count)
-            p = REGIONS ? base + ep::group_row(*g, e, m) * width + (off - (uint32_t)r * width)
-                        : base + (int64_t)step * 64 * width + off;
+        if (m < count) {
+            if constexpr (kTable)
+                p = base + looked_up(step, r) * width + (off - (uint32_t)r * width);
+            else if constexpr (REGIONS)
+                p = base + ep::group_row(*g, e, m) * width + (off - (uint32_t)r * width);
+            else
+                p = base + (int64_t)step * 64 * width + off;
+        }
         copy16(p, to);
     }
     struct Half {
@@ -937,8 +1125,14 @@ struct Wgrad {
                 for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
             if (count > 0) {
                 __syncthreads();  // the last tile's reads of the ring are done
-                reduce(Wgrad(a, e, count, n0, k0, wave, lane), lds_address(sh.ring), (count + 63) / 64,
-                       REGIONS ? 0 : count / 64, acc);
+                if constexpr (KEPT) {
+                    Wgrad w(a, e, count, n0, k0, wave, lane);
+                    if constexpr (kTable) w.kept.table = lds_address(sh.rows);
+                    reduce_kept(w, lds_address(sh.ring), (count + 63) / 64, REGIONS ? 0 : count / 64, acc);
+                } else {
+                    reduce(Wgrad(a, e, count, n0, k0, wave, lane), lds_address(sh.ring), (count + 63) / 64,
+                           REGIONS ? 0 : count / 64, acc);
+                }
             } else if (a.accumulate) {
                 continue;
             }
@@ -969,9 +1163,9 @@ struct Wgrad {
     }
 };
 
-template <int BM, int BN, int WM, int WN, bool REGIONS>
+template <int BM, int BN, int WM, int WN, bool REGIONS, bool KEPT>
 __global__ __launch_bounds__(WM *WN * 64, BN >= 256 ? 1 : 2) void k_wgrad(WgradArgs a) {
-    using P = Wgrad<BM, BN, WM, WN, REGIONS>;
+    using P = Wgrad<BM, BN, WM, WN, REGIONS, KEPT>;
     __shared__ typename P::Shared sh;
     P::body(a, sh);
 }
@@ -1007,12 +1201,12 @@ hipError_t launch_product_form(const ProductArgs &a, int64_t rows, int cus, hipS
     return launch_product<FORM, WTR, 128, 2, 2, 4>(a, (int)(most < 2 * cus ? most : 2 * cus), s);
 }
 
-template <int BM, int BN, int WM, int WN, bool REGIONS>
+template <int BM, int BN, int WM, int WN, bool REGIONS, bool KEPT>
 hipError_t launch_wgrad(const WgradArgs &a, int cus, hipStream_t s) {
     const int64_t tiles = (int64_t)a.g.E * ((a.N + BM - 1) / BM) * ((a.K + BN - 1) / BN);
     const int64_t most = (int64_t)cus * (BN >= 256 ? 1 : 2);
     const int grid = (int)(tiles < most ? tiles : most);
-    k_wgrad<BM, BN, WM, WN, REGIONS><<<grid, WM * WN * 64, 0, s>>>(a);
+    k_wgrad<BM, BN, WM, WN, REGIONS, KEPT><<<grid, WM * WN * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -1031,21 +1225,23 @@ int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const vo
                    const void *weight_scales, int K, int N, uint16_t *out, ep_stream_t stream) {
     ProductArgs a;
     if (int r = ep::group_args(groups, &a.g)) return r;
-    if (form != EP_FORM_BF16 && form != EP_FORM_FP8 && form != EP_FORM_MXFP4) return EP_ERR_ARG;
+    if (form != EP_FORM_BF16 && form != EP_FORM_FP8 && form != EP_FORM_MXFP4 && form != EP_FORM_INT8) return EP_ERR_ARG;
     if (bad_channels(K) || bad_channels(N)) return EP_ERR_ARG;
-    if (form != EP_FORM_BF16 && K % 128) return EP_ERR_ARG;
+    if ((form == EP_FORM_FP8 || form == EP_FORM_MXFP4) && K % 128) return EP_ERR_ARG;
+    if (form == EP_FORM_INT8 && K % 16) return EP_ERR_ARG;  // rows of whole 16 bytes
     if (ep::group_rows(groups) == 0) return EP_OK;
     if (!rows || !weights || !out) return EP_ERR_ARG;
     if ((form != EP_FORM_BF16) != (row_scales != nullptr) || (form != EP_FORM_BF16) != (weight_scales != nullptr))
         return EP_ERR_ARG;
     const size_t scale_align = form == EP_FORM_MXFP4 ? 16 : 4;
     if (misaligned(rows, 16) || misaligned(weights, 16) || misaligned(out, 16) || misaligned(row_scales, scale_align) ||
-        misaligned(weight_scales, scale_align))
+        misaligned(weight_scales, form == EP_FORM_INT8 ? 16 : scale_align))
         return EP_ERR_ALIGN;
     const int64_t all = ep::group_rows(groups), E = a.g.E;
-    const int64_t width = form == EP_FORM_BF16 ? K * 2 : form == EP_FORM_FP8 ? K : K / 2;
+    const int64_t width = form == EP_FORM_BF16 ? K * 2 : form == EP_FORM_MXFP4 ? K / 2 : K;
     if (far_regions(a.g, (int)width)) return EP_ERR_ARG;
-    const int64_t per_row = form == EP_FORM_FP8 ? K / 128 * 4 : K / 32, out_bytes = all * N * 2;  // a row's scales
+    // a row's scales
+    const int64_t per_row = form == EP_FORM_FP8 ? K / 128 * 4 : form == EP_FORM_INT8 ? 4 : K / 32, out_bytes = all * N * 2;
     if (ep::overlap(out, out_bytes, rows, all * width) || ep::overlap(out, out_bytes, weights, E * N * width) ||
         ep::overlap(out, out_bytes, row_scales, all * per_row) ||
         ep::overlap(out, out_bytes, weight_scales, E * (form == EP_FORM_FP8 ? (N + 127) / 128 : N) * per_row))
@@ -1067,6 +1263,10 @@ int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const vo
     if (form == EP_FORM_FP8) {
         a.steps = K / 128;
         return ep::hip_status(launch_product_form<kFp8, false>(a, n, cus, (hipStream_t)stream), "ep_expert_gemm");
+    }
+    if (form == EP_FORM_INT8) {
+        a.steps = (K + 127) / 128;
+        return ep::hip_status(launch_product_form<kInt8, false>(a, n, cus, (hipStream_t)stream), "ep_expert_gemm");
     }
     a.steps = (K + 255) / 256;
     return ep::hip_status(launch_product_form<kMx4, false>(a, n, cus, (hipStream_t)stream), "ep_expert_gemm");
@@ -1098,22 +1298,25 @@ int ep_expert_gemm_dgrad(const ep_groups *groups, const uint16_t *grad_out, cons
                           "ep_expert_gemm_dgrad");
 }
 
-int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, const uint16_t *rows, int K, int N,
-                         void *grad_weights, int out_f32, int accumulate, ep_stream_t stream) {
+// the weight gradient of bf16 rows, or (scales not NULL) of rows kept in MXINT8
+static int wgrad(const ep_groups *groups, const uint16_t *grad_out, const void *rows, const uint8_t *scales, bool kept,
+                 int K, int N, void *grad_weights, int out_f32, int accumulate, ep_stream_t stream, const char *name) {
     WgradArgs a;
     if (int r = ep::group_args(groups, &a.g)) return r;
-    if (bad_channels(K) || bad_channels(N)) return EP_ERR_ARG;
+    if (bad_channels(K) || bad_channels(N) || (kept && K % 32)) return EP_ERR_ARG;
     if (accumulate && !out_f32) return EP_ERR_ARG;
     if (!grad_weights) return EP_ERR_ARG;
-    if (ep::group_rows(groups) > 0 && (!grad_out || !rows)) return EP_ERR_ARG;
+    if (ep::group_rows(groups) > 0 && (!grad_out || !rows || (kept && !scales))) return EP_ERR_ARG;
     if (misaligned(grad_out, 16) || misaligned(rows, 16) || misaligned(grad_weights, 16)) return EP_ERR_ALIGN;
     const int64_t all = ep::group_rows(groups), out_bytes = (int64_t)a.g.E * N * K * (out_f32 ? 4 : 2);
     if (ep::overlap(grad_weights, out_bytes, grad_out, all * N * 2) ||
-        ep::overlap(grad_weights, out_bytes, rows, all * K * 2))
+        ep::overlap(grad_weights, out_bytes, rows, all * K * (kept ? 1 : 2)) ||
+        (kept && ep::overlap(grad_weights, out_bytes, scales, all * (K / 32))))
         return EP_ERR_ARG;
     int cus;
     if (int r = ep::device_cus(&cus)) return r;
     a.x = (const uint8_t *)rows;
+    a.x_scales = scales;
     a.grad = (const uint8_t *)grad_out;
     a.out = grad_weights;
     a.K = K;
@@ -1127,10 +1330,29 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
     const int64_t big = (int64_t)a.g.E * ((N + 255) / 256) * ((K + 255) / 256);
     const bool wide = big >= cus && ep::group_rows_expected(groups) >= 128 * (int64_t)a.g.E;
     const hipStream_t s = (hipStream_t)stream;
-    const hipError_t e = a.g.region_rows > 0 ? launch_wgrad<128, 128, 2, 2, true>(a, cus, s)
-                         : wide              ? launch_wgrad<256, 256, 2, 2, false>(a, cus, s)
-                                             : launch_wgrad<128, 128, 2, 2, false>(a, cus, s);
-    return ep::hip_status(e, "ep_expert_gemm_wgrad");
+    hipError_t e;
+    if (kept)
+        e = a.g.region_rows > 0 ? launch_wgrad<128, 128, 2, 2, true, true>(a, cus, s)
+            : wide              ? launch_wgrad<256, 256, 2, 2, false, true>(a, cus, s)
+                                : launch_wgrad<128, 128, 2, 2, false, true>(a, cus, s);
+    else
+        e = a.g.region_rows > 0 ? launch_wgrad<128, 128, 2, 2, true, false>(a, cus, s)
+            : wide              ? launch_wgrad<256, 256, 2, 2, false, false>(a, cus, s)
+                                : launch_wgrad<128, 128, 2, 2, false, false>(a, cus, s);
+    return ep::hip_status(e, name);
+}
+
+int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, const uint16_t *rows, int K, int N,
+                         void *grad_weights, int out_f32, int accumulate, ep_stream_t stream) {
+    return wgrad(groups, grad_out, rows, nullptr, false, K, N, grad_weights, out_f32, accumulate, stream,
+                 "ep_expert_gemm_wgrad");
+}
+
+int ep_expert_gemm_wgrad_mxint8(const ep_groups *groups, const uint16_t *grad_out, const int8_t *q,
+                                const uint8_t *scales, int K, int N, void *grad_weights, int out_f32, int accumulate,
+                                ep_stream_t stream) {
+    return wgrad(groups, grad_out, q, scales, true, K, N, grad_weights, out_f32, accumulate, stream,
+                 "ep_expert_gemm_wgrad_mxint8");
 }
 
 }  // extern "C"

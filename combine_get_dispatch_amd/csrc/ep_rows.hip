@@ -40,10 +40,12 @@ struct RowsArgs {
     int64_t cols;      // channels of one output row (I of SwiGLU)
     const uint16_t *a; // gate_up, or the values to quantize
     const uint16_t *d; // SwiGLU's grad_out
-    const uint8_t *q;  // dequantization
+    const uint8_t *q;  // dequantization, what SwiGLU kept
     const uint8_t *qs;
     void *out;
     void *scales;
+    uint8_t *keep;     // what SwiGLU keeps (its scales: scales)
+    uint16_t *again;   // SwiGLU of what was kept, or NULL
 };
 
 __device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
@@ -91,7 +93,10 @@ struct RowWalk {
     }
 };
 
-enum Op { kSwigluBf16, kSwigluFp8, kSwigluMx4, kSwigluGrad, kQuantize, kDequantize };
+enum Op {
+    kSwigluBf16, kSwigluFp8, kSwigluMx4, kSwigluGrad, kQuantize, kDequantize,
+    kQuantizeMx8, kDequantizeMx8, kSwigluKeep, kSwigluKeptGrad
+};
 
 constexpr int kPer = 8;     // channels per lane and chunk
 constexpr int kUnroll = 2;      // chunks whose loads are in flight together
@@ -102,7 +107,9 @@ constexpr int kBlocksPerCu = 64;
 
 // 16-byte vectors that a lane loads
 template <int OP>
-constexpr int kVecs = OP == kSwigluGrad ? 3 : OP == kQuantize || OP == kDequantize ? 1 : 2;
+constexpr int kVecs = OP == kSwigluGrad || OP == kSwigluKeptGrad                                       ? 3
+                      : OP == kQuantize || OP == kDequantize || OP == kQuantizeMx8 || OP == kDequantizeMx8 ? 1
+                                                                                                       : 2;
 
 __device__ __forceinline__ u32x4 load16(const void *p) { return __builtin_nontemporal_load((const u32x4 *)p); }
 template <class T>
@@ -139,13 +146,52 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&f)[8], uint8_t &scal
     return bad ? 0 : v;
 }
 
+// Eight MXINT8 codes of a lane and the scale byte of its four lanes' group.
+__device__ __forceinline__ u32x2 mx8_codes(const float (&f)[8], uint8_t &scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    top = max(top, from_lane<0xB1>(top));
+    top = max(top, from_lane<0x4E>(top));
+    const int field = (int)(top >> 23);  // as in mx4_codes; a bf16 subnormal's group: 0, which is 2^-127
+    const bool bad = field == 255;
+    scale = (uint8_t)field;
+    // x / 2^(field - 133), exact: bf16 values have 8 bits. A half of the power twice (each of them a normal number)
+    const int up = 133 - field;
+    const float a = __uint_as_float((uint32_t)(127 + up / 2) << 23), b = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float r = fminf(fmaxf(__builtin_rintf(f[i] * a * b), -127.0f), 127.0f);
+        q[i / 4] |= ((uint32_t)(int)r & 0xFF) << (8 * (i % 4));
+    }
+    return bad ? u32x2{0, 0} : u32x2{q[0], q[1]};
+}
+
+// 2^(b - 133), what a code of 1 stands for under the scale byte b (255: NaN)
+__device__ __forceinline__ float mx8_unit(uint32_t b) {
+    return b == 255 ? __builtin_nanf("") : __uint_as_float(b > 6 ? (b - 6) << 23 : 1u << (16 + b));
+}
+__device__ __forceinline__ float mx8_code(uint32_t word, int i) { return (float)((int)(word << (24 - 8 * i)) >> 24); }
+
 template <int OP>
 __device__ __forceinline__ void load_lane(const RowsArgs &a, int64_t row, int64_t c, u32x4 *v) {
     const int64_t at = row * a.cols + c;
     if constexpr (OP == kDequantize) {
         v[0].x = __builtin_nontemporal_load((const uint32_t *)(a.q + at / 2));
         v[0].y = a.qs[at / 32];
-    } else if constexpr (OP == kQuantize) {
+    } else if constexpr (OP == kDequantizeMx8) {
+        const u32x2 q = __builtin_nontemporal_load((const u32x2 *)(a.q + at));
+        v[0] = u32x4{q.x, q.y, a.qs[at / 32], 0};
+    } else if constexpr (OP == kSwigluKeptGrad) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // gate, up
+            const int64_t from = row * 2 * a.cols + h * a.cols + c;
+            const u32x2 q = __builtin_nontemporal_load((const u32x2 *)(a.q + from));
+            v[h] = u32x4{q.x, q.y, a.qs[from / 32], 0};
+        }
+        v[2] = load16(a.d + at);
+    } else if constexpr (OP == kQuantize || OP == kQuantizeMx8) {
         v[0] = load16(a.a + at);
     } else {
         const uint16_t *p = a.a + row * 2 * a.cols + c;
@@ -175,25 +221,43 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
             o[k] = pack_bf16(f[0], f[1]);
         }
         store(o, (uint16_t *)a.out + at);
-    } else if constexpr (OP == kSwigluGrad) {
-        u32x4 og, ou;
+    } else if constexpr (OP == kDequantizeMx8) {
+        const float unit = mx8_unit(v[0].z);
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = pack_bf16(mx8_code(v[0][k / 2], k % 2 * 2) * unit, mx8_code(v[0][k / 2], k % 2 * 2 + 1) * unit);
+        store(o, (uint16_t *)a.out + at);
+    } else if constexpr (OP == kSwigluGrad || OP == kSwigluKeptGrad) {
+        u32x4 og, ou, oh;
+        float unit[2];
+        if constexpr (OP == kSwigluKeptGrad) unit[0] = mx8_unit(v[0].z), unit[1] = mx8_unit(v[1].z);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            float dg[2], du[2];
+            float dg[2], du[2], y[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float g = h ? hi16(v[0][k]) : lo16(v[0][k]), u = h ? hi16(v[1][k]) : lo16(v[1][k]);
+                float g, u;
+                if constexpr (OP == kSwigluKeptGrad) {
+                    g = mx8_code(v[0][k / 2], k % 2 * 2 + h) * unit[0];
+                    u = mx8_code(v[1][k / 2], k % 2 * 2 + h) * unit[1];
+                } else {
+                    g = h ? hi16(v[0][k]) : lo16(v[0][k]), u = h ? hi16(v[1][k]) : lo16(v[1][k]);
+                }
                 const float d = h ? hi16(v[2][k]) : lo16(v[2][k]);
                 const float s = sigmoid(g), gs = g * s;
                 dg[h] = d * u * fmaf(gs, 1.0f - s, s);
                 du[h] = d * gs;
+                y[h] = gs * u;
             }
             og[k] = pack_bf16(dg[0], dg[1]);
             ou[k] = pack_bf16(du[0], du[1]);
+            oh[k] = pack_bf16(y[0], y[1]);
         }
         uint16_t *o = (uint16_t *)a.out + row * 2 * a.cols + c;
         store(og, o);
         store(ou, o + a.cols);
+        if (OP == kSwigluKeptGrad && a.again) store(oh, a.again + at);
     } else {
         float f[8];
 #pragma unroll
@@ -201,12 +265,28 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float g = h ? hi16(v[0][k]) : lo16(v[0][k]);
-                if constexpr (OP == kQuantize)
+                if constexpr (OP == kQuantize || OP == kQuantizeMx8)
                     f[2 * k + h] = g;
                 else
                     f[2 * k + h] = g * sigmoid(g) * (h ? hi16(v[1][k]) : lo16(v[1][k]));
             }
-        if constexpr (OP == kSwigluBf16) {
+        if constexpr (OP == kSwigluKeep) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // gate, up
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[2 * k] = lo16(v[i][k]), x[2 * k + 1] = hi16(v[i][k]);
+                const int64_t to = row * 2 * a.cols + i * a.cols + c;
+                uint8_t s;
+                store(mx8_codes(x, s), a.keep + to);
+                if ((threadIdx.x & 3) == 0) ((uint8_t *)a.scales)[to / 32] = s;
+            }
+        }
+        if constexpr (OP == kQuantizeMx8) {
+            uint8_t s;
+            store(mx8_codes(f, s), (uint8_t *)a.out + at);
+            if ((threadIdx.x & 3) == 0) ((uint8_t *)a.scales)[at / 32] = s;
+        } else if constexpr (OP == kSwigluBf16 || OP == kSwigluKeep) {
             store(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])},
                   (uint16_t *)a.out + at);
         } else if constexpr (OP == kSwigluMx4 || OP == kQuantize) {
@@ -292,6 +372,115 @@ hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) 
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit integers with one scale per row
+// ---------------------------------------------------------------------------
+
+// A wave has a row, C chunks of 512 channels of it in registers (a longer row
+// is read twice, C = 0): the scale needs the largest of all. SWIGLU: of
+// silu(gate) up in place of the values.
+template <int C, bool SWIGLU>
+__global__ __launch_bounds__(kThreads) void k_row_int8(RowsArgs a) {
+    __shared__ int ends[ep::kGroupsMaxExperts];
+    const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * (kThreads / 64);
+    RowWalk walk{&a.g, ends, 0, 0, 0, 0};
+    const int chunks = (int)((a.cols + 511) / 512);
+    for (int64_t entry = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)); entry < rows;
+         entry += waves) {
+        const int64_t row = a.grouped ? walk.row((int)entry) : entry;
+        const uint16_t *p = a.a + row * a.cols * (SWIGLU ? 2 : 1);
+        auto load = [&](int i, u32x4 (&v)[SWIGLU ? 2 : 1]) __attribute__((always_inline)) {
+            const int c = i * 512 + lane * 8;
+            const bool in = c < a.cols;
+#pragma unroll
+            for (int s = 0; s < (SWIGLU ? 2 : 1); ++s) v[s] = in ? load16(p + s * a.cols + c) : u32x4{0, 0, 0, 0};
+        };
+        auto values = [&](const u32x4 (&v)[SWIGLU ? 2 : 1], float (&f)[8]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float g = h ? hi16(v[0][k]) : lo16(v[0][k]);
+                    if constexpr (SWIGLU)
+                        f[2 * k + h] = g * sigmoid(g) * (h ? hi16(v[1][k]) : lo16(v[1][k]));
+                    else
+                        f[2 * k + h] = g;
+                }
+        };
+        float m = 0.0f, z = 0.0f;
+        auto largest = [&](const float (&f)[8]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m = fmaxf(m, fabsf(f[i]));
+                z = fmaf(f[i], 0.0f, z);  // NaN if any value is NaN or infinite
+            }
+        };
+        auto write = [&](int i, const float (&f)[8], float inv, bool bad) __attribute__((always_inline)) {
+            const int c = i * 512 + lane * 8;
+            uint32_t q[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                q[k / 4] |= ((uint32_t)(int)__builtin_rintf(f[k] * inv) & 0xFF) << (8 * (k % 4));
+            if (c < a.cols) store(bad ? u32x2{0, 0} : u32x2{q[0], q[1]}, (uint8_t *)a.out + row * a.cols + c);
+        };
+        float f[C > 0 ? C : 1][8];
+        if constexpr (C > 0) {
+            u32x4 v[C][SWIGLU ? 2 : 1];
+#pragma unroll
+            for (int i = 0; i < C; ++i) load(i, v[i]);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                values(v[i], f[i]);
+                largest(f[i]);
+            }
+        } else {
+            for (int i = 0; i < chunks; ++i) {
+                u32x4 v[SWIGLU ? 2 : 1];
+                load(i, v);
+                values(v, f[0]);
+                largest(f[0]);
+            }
+        }
+        if (z != z) m = __builtin_inff();
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+        const bool bad = m == __builtin_inff();
+        const float am = fmaxf(m, 1e-30f), inv = 127.0f / am;
+        if constexpr (C > 0) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) write(i, f[i], inv, bad);
+        } else {
+            for (int i = 0; i < chunks; ++i) {
+                u32x4 v[SWIGLU ? 2 : 1];
+                load(i, v);
+                values(v, f[0]);
+                write(i, f[0], inv, bad);
+            }
+        }
+        if (lane == 0) ((float *)a.scales)[row] = bad ? __builtin_nanf("") : am / 127.0f;
+    }
+}
+
+template <bool SWIGLU>
+hipError_t launch_row_int8(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
+    const int64_t blocks = (rows + kThreads / 64 - 1) / (kThreads / 64), most = (int64_t)cus * kBlocksPerCu;
+    const int grid = (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+    const int64_t chunks = (a.cols + 511) / 512;
+    if (chunks <= 2)
+        k_row_int8<2, SWIGLU><<<grid, kThreads, 0, s>>>(a);
+    else if (chunks <= 4)
+        k_row_int8<4, SWIGLU><<<grid, kThreads, 0, s>>>(a);
+    else if (chunks <= 8)
+        k_row_int8<8, SWIGLU><<<grid, kThreads, 0, s>>>(a);
+    else if (!SWIGLU && chunks <= 16)
+        k_row_int8<SWIGLU ? 0 : 16, SWIGLU><<<grid, kThreads, 0, s>>>(a);
+    else
+        k_row_int8<0, SWIGLU><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 // common checks of the row-wise calls; EP_OK with *rows = 0: nothing to do
@@ -302,6 +491,8 @@ int rows_args(const ep_groups *groups, int64_t num_rows, int64_t cols, RowsArgs 
     a->a = a->d = nullptr;
     a->q = a->qs = nullptr;
     a->out = a->scales = nullptr;
+    a->keep = nullptr;
+    a->again = nullptr;
     a->g = GroupArgs{};
     *rows = num_rows;
     if (num_rows < 0 || num_rows >= ((int64_t)1 << 31)) return EP_ERR_ARG;
@@ -379,15 +570,16 @@ int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows
     RowsArgs a;
     int64_t rows;
     int cus = 0;
-    if (form != EP_FORM_BF16 && form != EP_FORM_FP8 && form != EP_FORM_MXFP4) return EP_ERR_ARG;
-    if (I < 8 || I > 65536 || I % (form == EP_FORM_BF16 ? 8 : form == EP_FORM_FP8 ? 128 : 32)) return EP_ERR_ARG;
+    if (form != EP_FORM_BF16 && form != EP_FORM_FP8 && form != EP_FORM_MXFP4 && form != EP_FORM_INT8) return EP_ERR_ARG;
+    if (I < 8 || I > 65536 || I % (form == EP_FORM_BF16 ? 8 : form == EP_FORM_FP8 ? 128 : form == EP_FORM_INT8 ? 16 : 32))
+        return EP_ERR_ARG;
     if (int r = rows_args(groups, num_rows, I, &a, &rows)) return r;
     if (rows == 0) return EP_OK;
     if (!gate_up || !out || (form != EP_FORM_BF16) != (scales != nullptr)) return EP_ERR_ARG;
-    if (misaligned(gate_up, 16) || misaligned(out, 16) || misaligned(scales, form == EP_FORM_FP8 ? 4 : 1))
+    if (misaligned(gate_up, 16) || misaligned(out, 16) || misaligned(scales, form == EP_FORM_MXFP4 ? 1 : 4))
         return EP_ERR_ALIGN;
-    const int64_t n = num_rows * I, out_bytes = form == EP_FORM_BF16 ? n * 2 : form == EP_FORM_FP8 ? n : n / 2;
-    const int64_t scale_bytes = form == EP_FORM_FP8 ? n / 128 * 4 : n / 32;
+    const int64_t n = num_rows * I, out_bytes = form == EP_FORM_BF16 ? n * 2 : form == EP_FORM_MXFP4 ? n / 2 : n;
+    const int64_t scale_bytes = form == EP_FORM_FP8 ? n / 128 * 4 : form == EP_FORM_INT8 ? num_rows * 4 : n / 32;
     if (ep::overlap(out, out_bytes, gate_up, n * 4) || ep::overlap(scales, scale_bytes, gate_up, n * 4) ||
         ep::overlap(out, out_bytes, scales, scale_bytes))
         return EP_ERR_ARG;
@@ -398,7 +590,8 @@ int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows
     const hipStream_t s = (hipStream_t)stream;
     return ep::hip_status(form == EP_FORM_BF16  ? launch_rows<kSwigluBf16>(a, rows, cus, s)
                           : form == EP_FORM_FP8 ? launch_rows<kSwigluFp8>(a, rows, cus, s)
-                                                : launch_rows<kSwigluMx4>(a, rows, cus, s),
+                          : form == EP_FORM_INT8 ? launch_row_int8<true>(a, rows, cus, s)
+                                                 : launch_rows<kSwigluMx4>(a, rows, cus, s),
                           "ep_swiglu");
 }
 
@@ -468,6 +661,125 @@ int ep_dequantize_mxfp4(const ep_groups *groups, const uint8_t *q, const uint8_t
     a.qs = scales;
     a.out = x;
     return ep::hip_status(launch_rows<kDequantize>(a, rows, cus, (hipStream_t)stream), "ep_dequantize_mxfp4");
+}
+
+int ep_quantize_int8(const ep_groups *groups, const uint16_t *x, int64_t num_rows, int cols, int8_t *q, float *scales,
+                     ep_stream_t stream) {
+    RowsArgs a;
+    int64_t rows;
+    int cus = 0;
+    if (cols < 16 || cols > 65536 || cols % 16) return EP_ERR_ARG;
+    if (int r = rows_args(groups, num_rows, cols, &a, &rows)) return r;
+    if (rows == 0) return EP_OK;
+    if (!x || !q || !scales) return EP_ERR_ARG;
+    if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scales, 4)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * cols;
+    if (ep::overlap(q, n, x, n * 2) || ep::overlap(scales, num_rows * 4, x, n * 2) ||
+        ep::overlap(q, n, scales, num_rows * 4))
+        return EP_ERR_ARG;
+    if (int r = ep::device_cus(&cus)) return r;
+    a.a = x;
+    a.out = q;
+    a.scales = scales;
+    return ep::hip_status(launch_row_int8<false>(a, rows, cus, (hipStream_t)stream), "ep_quantize_int8");
+}
+
+int ep_quantize_mxint8(const ep_groups *groups, const uint16_t *x, int64_t num_rows, int cols, int8_t *q,
+                       uint8_t *scales, ep_stream_t stream) {
+    RowsArgs a;
+    int64_t rows;
+    int cus = 0;
+    if (cols < 32 || cols > 65536 || cols % 32) return EP_ERR_ARG;
+    if (int r = rows_args(groups, num_rows, cols, &a, &rows)) return r;
+    if (rows == 0) return EP_OK;
+    if (!x || !q || !scales) return EP_ERR_ARG;
+    if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * cols;
+    if (ep::overlap(q, n, x, n * 2) || ep::overlap(scales, n / 32, x, n * 2) || ep::overlap(q, n, scales, n / 32))
+        return EP_ERR_ARG;
+    if (int r = ep::device_cus(&cus)) return r;
+    if (!groups) {  // dense rows are one long one
+        a.cols = num_rows * cols;
+        a.num_rows = rows = 1;
+    }
+    a.a = x;
+    a.out = q;
+    a.scales = scales;
+    return ep::hip_status(launch_rows<kQuantizeMx8>(a, rows, cus, (hipStream_t)stream), "ep_quantize_mxint8");
+}
+
+int ep_dequantize_mxint8(const ep_groups *groups, const int8_t *q, const uint8_t *scales, int64_t num_rows, int cols,
+                         uint16_t *x, ep_stream_t stream) {
+    RowsArgs a;
+    int64_t rows;
+    int cus = 0;
+    if (cols < 32 || cols > 65536 || cols % 32) return EP_ERR_ARG;
+    if (int r = rows_args(groups, num_rows, cols, &a, &rows)) return r;
+    if (rows == 0) return EP_OK;
+    if (!x || !q || !scales) return EP_ERR_ARG;
+    if (misaligned(x, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * cols;
+    if (ep::overlap(x, n * 2, q, n) || ep::overlap(x, n * 2, scales, n / 32)) return EP_ERR_ARG;
+    if (int r = ep::device_cus(&cus)) return r;
+    if (!groups) {
+        a.cols = num_rows * cols;
+        a.num_rows = rows = 1;
+    }
+    a.q = (const uint8_t *)q;
+    a.qs = scales;
+    a.out = x;
+    return ep::hip_status(launch_rows<kDequantizeMx8>(a, rows, cus, (hipStream_t)stream), "ep_dequantize_mxint8");
+}
+
+int ep_swiglu_checkpoint(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows, int I, uint16_t *out,
+                         int8_t *q, uint8_t *scales, ep_stream_t stream) {
+    RowsArgs a;
+    int64_t rows;
+    int cus = 0;
+    if (I < 32 || I > 65536 || I % 32) return EP_ERR_ARG;
+    if (int r = rows_args(groups, num_rows, I, &a, &rows)) return r;
+    if (rows == 0) return EP_OK;
+    if (!gate_up || !out || !q || !scales) return EP_ERR_ARG;
+    if (misaligned(gate_up, 16) || misaligned(out, 16) || misaligned(q, 16)) return EP_ERR_ALIGN;
+    const int64_t n = num_rows * I;
+    if (ep::overlap(out, n * 2, gate_up, n * 4) || ep::overlap(q, n * 2, gate_up, n * 4) ||
+        ep::overlap(scales, n / 16, gate_up, n * 4) || ep::overlap(out, n * 2, q, n * 2) ||
+        ep::overlap(out, n * 2, scales, n / 16) || ep::overlap(q, n * 2, scales, n / 16))
+        return EP_ERR_ARG;
+    if (int r = ep::device_cus(&cus)) return r;
+    a.a = gate_up;
+    a.out = out;
+    a.keep = (uint8_t *)q;
+    a.scales = scales;
+    return ep::hip_status(launch_rows<kSwigluKeep>(a, rows, cus, (hipStream_t)stream), "ep_swiglu_checkpoint");
+}
+
+int ep_swiglu_checkpoint_backward(const ep_groups *groups, const uint16_t *grad_out, const int8_t *q,
+                                  const uint8_t *scales, int64_t num_rows, int I, uint16_t *grad_gate_up, uint16_t *out,
+                                  ep_stream_t stream) {
+    RowsArgs a;
+    int64_t rows;
+    int cus = 0;
+    if (I < 32 || I > 65536 || I % 32) return EP_ERR_ARG;
+    if (int r = rows_args(groups, num_rows, I, &a, &rows)) return r;
+    if (rows == 0) return EP_OK;
+    if (!grad_out || !q || !scales || !grad_gate_up) return EP_ERR_ARG;
+    if (misaligned(grad_out, 16) || misaligned(q, 16) || misaligned(grad_gate_up, 16) || misaligned(out, 16))
+        return EP_ERR_ALIGN;
+    const int64_t n = num_rows * I;
+    if (ep::overlap(grad_gate_up, n * 4, grad_out, n * 2) || ep::overlap(grad_gate_up, n * 4, q, n * 2) ||
+        ep::overlap(grad_gate_up, n * 4, scales, n / 16) || ep::overlap(out, n * 2, grad_out, n * 2) ||
+        ep::overlap(out, n * 2, q, n * 2) || ep::overlap(out, n * 2, scales, n / 16) ||
+        ep::overlap(out, n * 2, grad_gate_up, n * 4))
+        return EP_ERR_ARG;
+    if (int r = ep::device_cus(&cus)) return r;
+    a.q = (const uint8_t *)q;
+    a.qs = scales;
+    a.d = grad_out;
+    a.out = grad_gate_up;
+    a.again = out;
+    return ep::hip_status(launch_rows<kSwigluKeptGrad>(a, rows, cus, (hipStream_t)stream),
+                          "ep_swiglu_checkpoint_backward");
 }
 
 }  // extern "C"

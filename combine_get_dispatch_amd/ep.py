@@ -32,6 +32,10 @@ EP_ST_BAD_HANDLE = 16
 EP_FORM_BF16 = 0
 EP_FORM_FP8 = 1
 EP_FORM_MXFP4 = 2
+EP_FORM_INT8 = 4
+
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
 
 c_void_p = ctypes.c_void_p
 
@@ -72,7 +76,14 @@ class EpGroups(ctypes.Structure):
                 ("rows_hint", ctypes.c_int64)]
 
 
+class EpRouter(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("num_topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _GROUPS = ctypes.POINTER(EpGroups)
+_ROUTER = ctypes.POINTER(EpRouter)
 
 # (name, restype, argtypes) for every symbol include/ep.h declares
 SIGNATURES = {
@@ -139,6 +150,21 @@ SIGNATURES = {
                                          c_void_p]),
     "ep_dequantize_mxfp4": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p,
                                            c_void_p]),
+    "ep_quantize_int8": (ctypes.c_int, [_GROUPS, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p, c_void_p, c_void_p]),
+    "ep_quantize_mxint8": (ctypes.c_int, [_GROUPS, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p, c_void_p,
+                                          c_void_p]),
+    "ep_dequantize_mxint8": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p,
+                                            c_void_p]),
+    "ep_swiglu_checkpoint": (ctypes.c_int, [_GROUPS, c_void_p, ctypes.c_int64, ctypes.c_int, c_void_p, c_void_p,
+                                            c_void_p, c_void_p]),
+    "ep_swiglu_checkpoint_backward": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, c_void_p, ctypes.c_int64,
+                                                     ctypes.c_int, c_void_p, c_void_p, c_void_p]),
+    "ep_expert_gemm_wgrad_mxint8": (ctypes.c_int, [_GROUPS, c_void_p, c_void_p, c_void_p, ctypes.c_int, ctypes.c_int,
+                                                   c_void_p, ctypes.c_int, ctypes.c_int, c_void_p]),
+    "ep_route": (ctypes.c_int, [_ROUTER, c_void_p, ctypes.c_int, c_void_p, ctypes.c_int, c_void_p, c_void_p,
+                                c_void_p]),
+    "ep_route_backward": (ctypes.c_int, [_ROUTER, c_void_p, ctypes.c_int, c_void_p, c_void_p, ctypes.c_int, c_void_p,
+                                         c_void_p]),
 }
 
 _lib = None
@@ -375,6 +401,67 @@ def ep_dequantize_mxfp4(groups: Optional[EpGroups], q: int, scales: int, num_row
     if cols >> 31:
         _not_c_ints(cols)
     _check(load().ep_dequantize_mxfp4(_ref(groups), q, scales, num_rows, cols, x, stream), "ep_dequantize_mxfp4")
+
+
+def ep_quantize_int8(groups: Optional[EpGroups], x: int, num_rows: int, cols: int, q: int, scales: int,
+                     stream: int) -> None:
+    if cols >> 31:
+        _not_c_ints(cols)
+    _check(load().ep_quantize_int8(_ref(groups), x, num_rows, cols, q, scales, stream), "ep_quantize_int8")
+
+
+def ep_quantize_mxint8(groups: Optional[EpGroups], x: int, num_rows: int, cols: int, q: int, scales: int,
+                       stream: int) -> None:
+    if cols >> 31:
+        _not_c_ints(cols)
+    _check(load().ep_quantize_mxint8(_ref(groups), x, num_rows, cols, q, scales, stream), "ep_quantize_mxint8")
+
+
+def ep_dequantize_mxint8(groups: Optional[EpGroups], q: int, scales: int, num_rows: int, cols: int, x: int,
+                         stream: int) -> None:
+    if cols >> 31:
+        _not_c_ints(cols)
+    _check(load().ep_dequantize_mxint8(_ref(groups), q, scales, num_rows, cols, x, stream), "ep_dequantize_mxint8")
+
+
+def ep_swiglu_checkpoint(groups: Optional[EpGroups], gate_up: int, num_rows: int, I: int, out: int, q: int, scales: int,
+                         stream: int) -> None:
+    if I >> 31:
+        _not_c_ints(I)
+    _check(load().ep_swiglu_checkpoint(_ref(groups), gate_up, num_rows, I, out, q, scales, stream),
+           "ep_swiglu_checkpoint")
+
+
+def ep_swiglu_checkpoint_backward(groups: Optional[EpGroups], grad_out: int, q: int, scales: int, num_rows: int, I: int,
+                                  grad_gate_up: int, out: Optional[int], stream: int) -> None:
+    if I >> 31:
+        _not_c_ints(I)
+    _check(load().ep_swiglu_checkpoint_backward(_ref(groups), grad_out, q, scales, num_rows, I, grad_gate_up, out,
+                                                stream), "ep_swiglu_checkpoint_backward")
+
+
+def ep_expert_gemm_wgrad_mxint8(groups: EpGroups, grad_out: int, q: int, scales: int, K: int, N: int, grad_weights: int,
+                                out_f32: bool, accumulate: bool, stream: int) -> None:
+    if (K | N) >> 31:
+        _not_c_ints(K, N)
+    _check(load().ep_expert_gemm_wgrad_mxint8(_ref(groups), grad_out, q, scales, K, N, grad_weights, int(out_f32),
+                                              int(accumulate), stream), "ep_expert_gemm_wgrad_mxint8")
+
+
+def ep_route(router: EpRouter, logits: int, logits_f32: bool, bias: Optional[int], num_tokens: int, topk_idx: int,
+             topk_weights: int, stream: int) -> None:
+    if num_tokens >> 31:
+        _not_c_ints(num_tokens)
+    _check(load().ep_route(ctypes.byref(router), logits, int(logits_f32), bias, num_tokens, topk_idx, topk_weights,
+                           stream), "ep_route")
+
+
+def ep_route_backward(router: EpRouter, logits: int, logits_f32: bool, topk_idx: int, grad_weights: int,
+                      num_tokens: int, grad_logits: int, stream: int) -> None:
+    if num_tokens >> 31:
+        _not_c_ints(num_tokens)
+    _check(load().ep_route_backward(ctypes.byref(router), logits, int(logits_f32), topk_idx, grad_weights, num_tokens,
+                                    grad_logits, stream), "ep_route_backward")
 
 
 # ---------------------------------------------------------------------------
@@ -787,6 +874,8 @@ def expert_gemm(rows, weights, groups: Groups, row_scales=None, weight_scales=No
       MXFP4  rows [R*cap_rows, K/2], weights [E, N, K/2] uint8; uint8
              row_scales [R*cap_rows, K/32], weight_scales [E, N, K/32]
              (quantize_mxfp4 writes both)
+      INT8   rows [R*cap_rows, K], weights [E, N, K] int8; float32 row_scales
+             [R*cap_rows] and weight_scales [E, N] (quantize_int8 writes both)
     """
     dev = _device()
     g = groups._c(dev)
@@ -796,6 +885,10 @@ def expert_gemm(rows, weights, groups: Groups, row_scales=None, weight_scales=No
         raise EpError(EP_ERR_ARG, "rows and weights need scales both, or neither")
     if row_scales is None:
         form, K, dtype, rs, ws = EP_FORM_BF16, width, _torch.bfloat16, None, None
+    elif weights.dtype == _torch.int8:
+        form, K, dtype = EP_FORM_INT8, width, _torch.int8
+        rs = _tensor(row_scales, "row_scales", _torch.float32, (n,), dev)
+        ws = _tensor(weight_scales, "weight_scales", _torch.float32, (groups.num_experts, N), dev)
     elif row_scales.dtype == _torch.float32:
         form, K, dtype = EP_FORM_FP8, width, _torch.uint8
         rs = _tensor(row_scales, "row_scales", _torch.float32, (n, K // 128), dev)
@@ -828,11 +921,13 @@ def expert_gemm_dgrad(grad_out, weights, groups: Groups, out=None):
     return out
 
 
-def expert_gemm_wgrad(grad_out, rows, groups: Groups, out=None, dtype=None, accumulate: bool = False):
+def expert_gemm_wgrad(grad_out, rows, groups: Groups, out=None, dtype=None, accumulate: bool = False,
+                      row_scales=None):
     """Gradient of the bf16 ``expert_gemm`` in its weights: grad_out
     [R*cap_rows, N], rows [R*cap_rows, K] bfloat16 -> [E, N, K] of ``dtype``
     (float32, the default, or bfloat16; ``out``'s own where it is given).
-    ``accumulate`` adds to a float32 ``out``."""
+    ``accumulate`` adds to a float32 ``out``. With ``row_scales`` (uint8
+    [R*cap_rows, K/32]) the rows are int8, as quantize_mxint8 kept them."""
     dev = _device()
     g = groups._c(dev)
     n, N = _shape(grad_out, "grad_out", 2)
@@ -845,12 +940,16 @@ def expert_gemm_wgrad(grad_out, rows, groups: Groups, out=None, dtype=None, accu
     if dtype not in (_torch.float32, _torch.bfloat16):
         raise EpError(EP_ERR_ARG, f"weight gradients are float32 or bfloat16, not {dtype}")
     d = _tensor(grad_out, "grad_out", _torch.bfloat16, (groups.num_rows, N), dev)
-    x = _tensor(rows, "rows", _torch.bfloat16, (groups.num_rows, K), dev)
+    x = _tensor(rows, "rows", _torch.bfloat16 if row_scales is None else _torch.int8, (groups.num_rows, K), dev)
+    s = None if row_scales is None else _tensor(row_scales, "row_scales", _torch.uint8, (groups.num_rows, K // 32), dev)
     shape = (groups.num_experts, N, K)
     if out is None:
         out = _torch.empty(shape, dtype=dtype, device=rows.device)
-    ep_expert_gemm_wgrad(g, d, x, K, N, _tensor(out, "out", dtype, shape, dev), dtype == _torch.float32, accumulate,
-                         _raw_stream(dev))
+    o = _tensor(out, "out", dtype, shape, dev)
+    if s is None:
+        ep_expert_gemm_wgrad(g, d, x, K, N, o, dtype == _torch.float32, accumulate, _raw_stream(dev))
+    else:
+        ep_expert_gemm_wgrad_mxint8(g, d, x, s, K, N, o, dtype == _torch.float32, accumulate, _raw_stream(dev))
     return out
 
 
@@ -858,8 +957,9 @@ def swiglu(gate_up, groups: Optional[Groups] = None, kind: str = "bf16", out=Non
     """silu(gate) * up of rows [num_rows, 2*I] bfloat16 (gate first), between
     the experts' two products. ``kind`` "bf16" returns [num_rows, I] bfloat16;
     "fp8" (uint8 e4m3 [num_rows, I], float32 scales [num_rows, I/128]) and
-    "mxfp4" (uint8 [num_rows, I/2], uint8 scales [num_rows, I/32]) return what
-    the next ``expert_gemm`` reads; ``out`` is of the same form. With
+    "mxfp4" (uint8 [num_rows, I/2], uint8 scales [num_rows, I/32]) and "int8"
+    (int8 [num_rows, I], float32 scales [num_rows]) return what the next
+    ``expert_gemm`` reads; ``out`` is of the same form. With
     ``groups`` only the rows experts have are computed and written."""
     dev = _device()
     n, I = _shape(gate_up, "gate_up", 2)
@@ -871,8 +971,10 @@ def swiglu(gate_up, groups: Optional[Groups] = None, kind: str = "bf16", out=Non
         form, spec = EP_FORM_FP8, (((n, I), _torch.uint8), ((n, I // 128), _torch.float32))
     elif kind == "mxfp4":
         form, spec = EP_FORM_MXFP4, (((n, I // 2), _torch.uint8), ((n, I // 32), _torch.uint8))
+    elif kind == "int8":
+        form, spec = EP_FORM_INT8, (((n, I), _torch.int8), ((n,), _torch.float32))
     else:
-        raise EpError(EP_ERR_ARG, f"kind {kind!r} is none of bf16, fp8, mxfp4")
+        raise EpError(EP_ERR_ARG, f"kind {kind!r} is none of bf16, fp8, mxfp4, int8")
     outs = (out,) if kind == "bf16" and out is not None else out
     if outs is None:
         outs = tuple(_torch.empty(s, dtype=t, device=gate_up.device) for s, t in spec)
@@ -925,6 +1027,172 @@ def dequantize_mxfp4(q, scales, groups: Optional[Groups] = None, out=None):
         out = _torch.empty(shape, dtype=_torch.bfloat16, device=q.device)
     ep_dequantize_mxfp4(None if groups is None else groups._c(dev), p, s, n, cols,
                         _tensor(out, "out", _torch.bfloat16, shape, dev), _raw_stream(dev))
+    return out
+
+
+def _quantized(x, groups, out, call, dtype, scale_shape, scale_dtype):
+    """``call`` on the bfloat16 rows of x [..., cols] to ``dtype`` values and scales."""
+    dev = _device()
+    cols = x.shape[-1] if x.dim() else 0
+    n = x.numel() // cols if cols else 0
+    p = _tensor(x, "x", _torch.bfloat16, x.shape, dev)
+    shape = tuple(x.shape)
+    scale_shape = scale_shape(shape) if shape else ()
+    if out is None:
+        out = _torch.empty(shape, dtype=dtype, device=x.device), _torch.empty(scale_shape, dtype=scale_dtype,
+                                                                              device=x.device)
+    q, scales = out
+    call(None if groups is None else groups._c(dev), p, n, cols, _tensor(q, "q", dtype, shape, dev),
+         _tensor(scales, "scales", scale_dtype, scale_shape, dev), _raw_stream(dev))
+    return q, scales
+
+
+def quantize_int8(x, groups: Optional[Groups] = None, out=None):
+    """The bfloat16 rows of x [..., cols] (rows of a product, or weights [E, N,
+    K]) as 8-bit integers with one scale each, for ``expert_gemm``: (int8 [...,
+    cols], float32 scales [...]). With ``groups`` (x [R*cap_rows, cols]) only
+    the rows experts have."""
+    _device()  # (binds torch)
+    return _quantized(x, groups, out, ep_quantize_int8, _torch.int8, lambda s: s[:-1], _torch.float32)
+
+
+def quantize_mxint8(x, groups: Optional[Groups] = None, out=None):
+    """An 8-bit checkpoint of the bfloat16 rows of x [..., cols], MXINT8: (int8
+    [..., cols], uint8 scales [..., cols/32]). With ``groups`` (x [R*cap_rows,
+    cols]) only the rows experts have. ``expert_gemm_wgrad`` reads it as it is."""
+    _device()  # (binds torch)
+    return _quantized(x, groups, out, ep_quantize_mxint8, _torch.int8, lambda s: s[:-1] + (s[-1] // 32,),
+                      _torch.uint8)
+
+
+def dequantize_mxint8(q, scales, groups: Optional[Groups] = None, out=None):
+    """The bfloat16 values [..., cols] that quantize_mxint8's (q, scales) stand for."""
+    dev = _device()
+    cols = q.shape[-1] if q.dim() else 0
+    n = q.numel() // cols if cols else 0
+    shape = tuple(q.shape)
+    p = _tensor(q, "q", _torch.int8, shape, dev)
+    s = _tensor(scales, "scales", _torch.uint8, shape[:-1] + (cols // 32,), dev)
+    if out is None:
+        out = _torch.empty(shape, dtype=_torch.bfloat16, device=q.device)
+    ep_dequantize_mxint8(None if groups is None else groups._c(dev), p, s, n, cols,
+                         _tensor(out, "out", _torch.bfloat16, shape, dev), _raw_stream(dev))
+    return out
+
+
+def swiglu_checkpoint(gate_up, groups: Optional[Groups] = None, out=None, kept=None):
+    """``swiglu`` to bfloat16 that keeps an 8-bit checkpoint of its input for
+    the backward pass: (h [num_rows, I] bfloat16, q int8 [num_rows, 2*I], uint8
+    scales [num_rows, 2*I/32]); ``out`` and ``kept`` = (q, scales) may be given.
+    Then gate_up need not be held."""
+    dev = _device()
+    n, I = _shape(gate_up, "gate_up", 2)
+    I //= 2
+    x = _tensor(gate_up, "gate_up", _torch.bfloat16, (n, 2 * I), dev)
+    if out is None:
+        out = _torch.empty((n, I), dtype=_torch.bfloat16, device=gate_up.device)
+    if kept is None:
+        kept = (_torch.empty((n, 2 * I), dtype=_torch.int8, device=gate_up.device),
+                _torch.empty((n, I // 16), dtype=_torch.uint8, device=gate_up.device))
+    q, scales = kept
+    ep_swiglu_checkpoint(None if groups is None else groups._c(dev), x, n, I,
+                         _tensor(out, "out", _torch.bfloat16, (n, I), dev), _tensor(q, "q", _torch.int8, (n, 2 * I), dev),
+                         _tensor(scales, "scales", _torch.uint8, (n, I // 16), dev), _raw_stream(dev))
+    return out, q, scales
+
+
+def swiglu_checkpoint_backward(grad_out, q, scales, groups: Optional[Groups] = None, out=None, again: bool = True):
+    """Gradient of ``swiglu_checkpoint`` from what it kept: grad_out [num_rows,
+    I] bfloat16 -> (grad_gate_up [num_rows, 2*I], h [num_rows, I]) bfloat16, h
+    the forward result of the kept values, the second product's rows (with
+    ``again`` False grad_gate_up alone); ``out`` is of the same form."""
+    dev = _device()
+    n, I = _shape(grad_out, "grad_out", 2)
+    d = _tensor(grad_out, "grad_out", _torch.bfloat16, (n, I), dev)
+    c = _tensor(q, "q", _torch.int8, (n, 2 * I), dev)
+    s = _tensor(scales, "scales", _torch.uint8, (n, I // 16), dev)
+    if out is None:
+        grad = _torch.empty((n, 2 * I), dtype=_torch.bfloat16, device=grad_out.device)
+        h = _torch.empty((n, I), dtype=_torch.bfloat16, device=grad_out.device) if again else None
+    else:
+        grad, h = out if again else (out, None)
+    ep_swiglu_checkpoint_backward(None if groups is None else groups._c(dev), d, c, s, n, I,
+                                  _tensor(grad, "grad_gate_up", _torch.bfloat16, (n, 2 * I), dev),
+                                  _tensor(h, "h", _torch.bfloat16, (n, I), dev) if again else None, _raw_stream(dev))
+    return (grad, h) if again else grad
+
+
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+
+
+@dataclass
+class Router:
+    """How a token's experts and weights come from its gate's logits (ep_router
+    in include/ep.h): softmax or sigmoid scores, the ``num_topk`` largest of
+    score plus bias, of the ``topk_groups`` best of ``num_groups`` groups of
+    neighbouring experts (a group's value: its largest, or the sum of its
+    ``group_top`` = 2 largest), weights the scores times ``scale``, divided by
+    their sum if ``renormalize``."""
+    num_experts: int
+    num_topk: int
+    score: str = "softmax"
+    renormalize: bool = True
+    scale: float = 1.0
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 2
+
+    def c(self) -> EpRouter:
+        if self.score not in _SCORES:
+            raise EpError(EP_ERR_ARG, f"score {self.score!r} is neither softmax nor sigmoid")
+        sizes = (self.num_experts, self.num_topk, self.num_groups, self.topk_groups, self.group_top)
+        if any(s >> 31 for s in sizes):
+            _not_c_ints(*sizes)
+        return EpRouter(self.num_experts, self.num_topk, _SCORES[self.score], int(bool(self.renormalize)),
+                        self.num_groups, self.topk_groups, self.group_top, self.scale)
+
+
+def _logits(logits, router: Router, dev: int):
+    T, _ = _shape(logits, "logits", 2)
+    if logits.dtype not in (_torch.float32, _torch.bfloat16):
+        raise EpError(EP_ERR_ARG, f"logits are float32 or bfloat16, not {logits.dtype}")
+    return T, _tensor(logits, "logits", logits.dtype, (T, router.num_experts), dev)
+
+
+def route(logits, router: Router, bias=None, out=None):
+    """The experts and weights of every token from the gate's logits [T, E]
+    (float32 or bfloat16), ready for the dispatch calls: (topk_idx [T, k] int32,
+    -1 where fewer than k experts are open to a token, topk_weights [T, k]
+    float32). ``bias`` [E] float32 takes part in the choice, not in the weights."""
+    dev = _device()
+    r = router.c()
+    T, p = _logits(logits, router, dev)
+    b = None if bias is None else _tensor(bias, "bias", _torch.float32, (router.num_experts,), dev)
+    shape = (T, router.num_topk)
+    if out is None:
+        out = (_torch.empty(shape, dtype=_torch.int32, device=logits.device),
+               _torch.empty(shape, dtype=_torch.float32, device=logits.device))
+    idx, w = out
+    ep_route(r, p, logits.dtype is _torch.float32, b, T, _tensor(idx, "topk_idx", _torch.int32, shape, dev),
+             _tensor(w, "topk_weights", _torch.float32, shape, dev), _raw_stream(dev))
+    return idx, w
+
+
+def route_backward(grad_weights, logits, topk_idx, router: Router, out=None):
+    """Gradient of ``route``'s weights in the logits: grad_weights [T, k]
+    float32, logits [T, E] and topk_idx [T, k] as in the forward call ->
+    [T, E] of the logits' type (``Buffer.combine``'s weights have the gradient
+    <expert_out row, grad_combined row>)."""
+    dev = _device()
+    r = router.c()
+    T, p = _logits(logits, router, dev)
+    shape = (T, router.num_topk)
+    d = _tensor(grad_weights, "grad_weights", _torch.float32, shape, dev)
+    idx = _tensor(topk_idx, "topk_idx", _torch.int32, shape, dev)
+    if out is None:
+        out = _torch.empty_like(logits)
+    ep_route_backward(r, p, logits.dtype is _torch.float32, idx, d, T,
+                      _tensor(out, "out", logits.dtype, logits.shape, dev), _raw_stream(dev))
     return out
 
 

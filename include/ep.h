@@ -460,6 +460,7 @@ typedef struct {
 #define EP_FORM_BF16 0
 #define EP_FORM_FP8 1   /* e4m3fn bytes, fp32 scales: rows one per 128 channels, weights one per 128 x 128 block */
 #define EP_FORM_MXFP4 2 /* e2m1 values, two per byte (the even channel in the low half), e8m0 scales per 32 channels */
+#define EP_FORM_INT8 4  /* 8-bit integers, fp32 scales: rows one each, weights one per output channel */
 
 /* Grouped product: for every row p of expert e and n < N,
  *   out[p][n] = bf16_rne(sum_k W[e][n][k] * row[p][k]),
@@ -474,8 +475,12 @@ typedef struct {
  *   MXFP4: rows [R*cap_rows][K/2] and weights [E][N][K/2] bytes with scales
  *     [..][K/32] bytes, a scale byte b standing for 2^(b-127), 255 for NaN
  *     (ep_quantize_mxfp4 writes both).
- * out: [R*cap_rows][N]. Rows, weights, out and MXFP4
- * scales 16-byte aligned, FP8 scales 4-byte. */
+ *   INT8: rows [R*cap_rows][K] and weights [E][N][K] int8 (K % 16 == 0), row_scales
+ *     [R*cap_rows] and weight_scales [E][N] fp32 (ep_quantize_int8 writes rows
+ *     and weights): out = bf16_rne(sum * (row scale * weight scale)), the sum
+ *     in 32-bit integers, exact, its conversion and both products in fp32.
+ * out: [R*cap_rows][N]. Rows, weights, out, MXFP4 scales and INT8 weight scales
+ * 16-byte aligned, the other scales 4-byte. */
 int ep_expert_gemm(const ep_groups *groups, int form, const void *rows, const void *row_scales, const void *weights,
                    const void *weight_scales, int K, int N, uint16_t *out, ep_stream_t stream);
 
@@ -505,6 +510,8 @@ int ep_expert_gemm_wgrad(const ep_groups *groups, const uint16_t *grad_out, cons
  *     gets a NaN scale and NaN codes.
  *   EP_FORM_MXFP4: out bytes [num_rows][I/2], scales bytes [num_rows][I/32], by
  *     ep_quantize_mxfp4's rule (I % 32 == 0).
+ *   EP_FORM_INT8: out int8 [num_rows][I], scales fp32 [num_rows], by
+ *     ep_quantize_int8's rule (I % 16 == 0).
  * h is not rounded to bf16 before it is quantized. 16-byte alignment. */
 int ep_swiglu(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows, int I, int form, void *out,
               void *scales, ep_stream_t stream);
@@ -529,6 +536,112 @@ int ep_quantize_mxfp4(const ep_groups *groups, const uint16_t *x, int64_t num_ro
                       uint8_t *scales, ep_stream_t stream);
 int ep_dequantize_mxfp4(const ep_groups *groups, const uint8_t *q, const uint8_t *scales, int64_t num_rows, int cols,
                         uint16_t *x, ep_stream_t stream);
+
+/* 8-bit integers with one scale per row, of bf16 rows x [num_rows][cols]
+ * (cols % 16 == 0): a = max(max |x|, 1e-30), scales[p] = a / 127 and
+ * q = rne(x * (127 / a)) (fp32 divisions and multiply, IEEE; ties to even). A
+ * row that holds a NaN or an infinity gets a NaN scale and zero codes. q:
+ * [num_rows][cols] int8, scales: [num_rows] fp32. groups NULL: every row (of
+ * weights [E][N][K] too: E*N rows); else the rows experts have (num_rows =
+ * R*cap_rows). x and q 16-byte aligned. */
+int ep_quantize_int8(const ep_groups *groups, const uint16_t *x, int64_t num_rows, int cols, int8_t *q, float *scales,
+                     ep_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits: what the backward pass needs of the experts'
+ * activations, kept at 8.25 bits a value (MXINT8) in place of 16. Values that a
+ * checkpoint stands for are bf16 numbers, so every use of one sees the same.
+ *
+ * MXINT8: per 32 channels e = floor(log2(max |x|)) (at least -127; zeros: -127),
+ * scale byte e + 127, and each value x / 2^(e-6) rounded to a whole number (ties
+ * to even), at most 127 in magnitude: off by at most half a step, 2^(e-7), for
+ * bf16 values. A group that holds a NaN or an infinity gets the scale byte 255
+ * (NaN) and zero codes. Code c under the scale byte b stands for c * 2^(b-133).
+ *
+ * ep_quantize_mxint8: bf16 rows x [num_rows][cols] (cols % 32 == 0) to q int8
+ * [num_rows][cols] and scales bytes [num_rows][cols/32]; ep_dequantize_mxint8 is
+ * the way back, exact. groups, num_rows and alignment (x, q: 16 bytes) as for
+ * ep_quantize_mxfp4. */
+int ep_quantize_mxint8(const ep_groups *groups, const uint16_t *x, int64_t num_rows, int cols, int8_t *q,
+                       uint8_t *scales, ep_stream_t stream);
+int ep_dequantize_mxint8(const ep_groups *groups, const int8_t *q, const uint8_t *scales, int64_t num_rows, int cols,
+                         uint16_t *x, ep_stream_t stream);
+
+/* SwiGLU that keeps its input: out [num_rows][I] bf16 as ep_swiglu writes it, and
+ * gate_up in MXINT8: q int8 [num_rows][2*I], scales bytes [num_rows][2*I/32]
+ * (I % 32 == 0), as ep_quantize_mxint8 writes them, in one pass. 16-byte
+ * alignment but for the scales. */
+int ep_swiglu_checkpoint(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows, int I, uint16_t *out,
+                         int8_t *q, uint8_t *scales, ep_stream_t stream);
+
+/* Its gradient from what was kept: grad_gate_up [num_rows][2*I] as
+ * ep_swiglu_backward of the kept values, and, where out is not NULL, their
+ * SwiGLU again, out [num_rows][I] (the second product's rows, whose weight
+ * gradient needs them). */
+int ep_swiglu_checkpoint_backward(const ep_groups *groups, const uint16_t *grad_out, const int8_t *q,
+                                  const uint8_t *scales, int64_t num_rows, int I, uint16_t *grad_gate_up, uint16_t *out,
+                                  ep_stream_t stream);
+
+/* ep_expert_gemm_wgrad of rows kept in MXINT8: q int8 [R*cap_rows][K] and scales
+ * bytes [R*cap_rows][K/32] (K % 32 == 0). The same sums as of the bf16 rows that
+ * they stand for. q 16-byte aligned, the other arguments as there. */
+int ep_expert_gemm_wgrad_mxint8(const ep_groups *groups, const uint16_t *grad_out, const int8_t *q,
+                                const uint8_t *scales, int K, int N, void *grad_weights, int out_f32, int accumulate,
+                                ep_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The router: which experts a token goes to and with which weights, from the
+ * gate's logits; what it writes is what the dispatch calls read. No context, no
+ * workspace, nothing allocated, any stream, capturable. Outputs share no memory
+ * with inputs or each other (EP_ERR_ARG).
+ *
+ * s_e: softmax of the token's logits over all experts, or sigmoid of each logit.
+ * Experts are chosen by c_e = s_e + bias_e (bias NULL: s_e): of num_groups groups
+ * of neighbouring experts the topk_groups with the largest value stay (a group's
+ * value: its largest c_e, or the sum of its two largest, group_top 1 or 2), and
+ * of their experts the num_topk with the largest c_e, in that order. Ties go to
+ * the lower index, of groups and of experts. The order is that of the exact
+ * scores: without a bias the logits are compared, with one 64-bit c_e, of which
+ * the leading 43 bits count; groups' sums are 64-bit numbers.
+ * Weights: w = scale * s_e of the chosen (the bias takes no part), divided by
+ * their sum if renormalize.
+ * An expert with a logit or a bias of -infinity or NaN is never chosen; a token
+ * that has fewer than num_topk experts open to it gets index -1 and weight 0 in
+ * its last slots (all, where every logit is -infinity). A NaN logit makes the
+ * weights of its token NaN. Experts whose logit is +infinity share softmax's sum.
+ * Limits: 1 <= num_experts <= 1024, 1 <= num_topk <= 32, num_topk <= topk_groups *
+ * (num_experts / num_groups), 1 <= num_groups <= 64, num_experts % num_groups == 0,
+ * 1 <= topk_groups <= num_groups; scale finite; 0 <= num_tokens <= 2^24. */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+typedef struct {
+    int32_t num_experts; /* E */
+    int32_t num_topk;    /* k */
+    int32_t score;       /* EP_SCORE_* */
+    int32_t renormalize; /* 0 or 1 */
+    int32_t num_groups;  /* 1: no groups */
+    int32_t topk_groups;
+    int32_t group_top;   /* 1 or 2 */
+    float scale;
+} ep_router;
+
+/* logits: [T][E] fp32 (logits_f32 = 1) or bf16; bias: [E] fp32 or NULL; topk_idx:
+ * [T][k] int32; topk_weights: [T][k] fp32; each aligned to its type. */
+int ep_route(const ep_router *router, const void *logits, int logits_f32, const float *bias, int num_tokens,
+             int32_t *topk_idx, float *topk_weights, ep_stream_t stream);
+
+/* Gradient of the weights in the logits: grad_logits [T][E], of the logits' type,
+ * for grad_weights [T][k] and the choice topk_idx [T][k] that ep_route made (which
+ * has no gradient itself). With d_j = scale * grad_weights[j] over the chosen j:
+ *   sigmoid:               d_j s_j (1 - s_j)
+ *   sigmoid, renormalized: p_j (1 - s_j) (d_j - sum_i p_i d_i), p_j = s_j / sum_i s_i
+ *   softmax, renormalized: p_j (d_j - sum_i p_i d_i)
+ *   softmax:               s_e (d_e - sum_i s_i d_i) for every expert, d_e = 0 where
+ *                          it is not chosen
+ * and 0 for the other experts. A slot whose index is outside [0, E), or that
+ * repeats an earlier one of its token, is left out. */
+int ep_route_backward(const ep_router *router, const void *logits, int logits_f32, const int32_t *topk_idx,
+                      const float *grad_weights, int num_tokens, void *grad_logits, ep_stream_t stream);
 
 #ifdef __cplusplus
 }
