@@ -366,29 +366,35 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
 
 // The reduction of a weight gradient whose rows' side is kept in 8 bits: as
 // above, with two buffers, but for that side, which a copy to LDS cannot widen.
-// Its codes are loaded to registers when a buffer has been read out (fetch),
-// widened and written to LDS in the next step's first half, a word of four
-// between four matrix instructions (put), and read from the step's middle on.
-// (The compiler waits for these loads by itself; it counts no copies to LDS, and
-// so waits for no less than it has to.)
+// Its codes are in registers a step ahead: in a step's first half they are
+// widened and written to the next step's buffer, a code between two matrix
+// instructions (put), and a chunk that is done with is loaded again for the step
+// after (fetch). The vector instructions that this takes, 200 a step and wave,
+// are what it costs beside the bf16 form (1.7 against 1.5 ms): at their full rate
+// the matrix instructions leave a wave's others no time of their own. So a copy
+// of the codes to LDS first, all waits counted by hand, was no faster (1.83 ms),
+// nor were the same instructions spread over both halves (1.85). (The compiler
+// waits for the loads by itself. It counts no copies to LDS, and so waits for no
+// less than it has to: for a chunk's loads it asks that no more be in flight
+// than there are later loads.)
 template <class P>
 __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
-    constexpr int ACT = P::ACT, NT = P::NT;
+    constexpr int ACT = P::ACT, NT = P::NT, C = P::kPer, W = 16 * P::kChunks;
     static_assert(P::kStages == 2, "two buffers");
     const uint32_t other = ring + P::kStage;
     if constexpr (P::kTable) {
-        p.look_up(0);
-        p.look_up(1);
+        for (int i = 0; i < 3; ++i) p.look_up(i);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (0 < whole) p.template fetch<true>(0); else p.template fetch<false>(0);
-    copy_step(p, ring, 0, whole, 0, P::kPer);
+    auto first = [&](int step, uint32_t stage) __attribute__((always_inline)) {
 #pragma unroll
-    for (int w = 0; w < P::kWords; ++w) p.put(ring, w);
-    if (1 < steps) {
-        if (1 < whole) p.template fetch<true>(1); else p.template fetch<false>(1);
-        copy_step(p, other, 1, whole, 0, P::kPer);
-    }
+        for (int i = 0; i < P::kChunks; ++i) p.template fetch<false>(step, i);
+        copy_step(p, stage, step, whole, 0, C);
+    };
+    first(0, ring);
+#pragma unroll
+    for (int c = 0; c < W; ++c) p.put(ring, c);
+    if (1 < steps) first(1, other);
     wait_copies<0>();
     typename P::Frags h0, h1;
 #pragma unroll
@@ -397,9 +403,9 @@ __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int 
     uint32_t st = ring, nx = other;
     auto body = [&](auto copies) __attribute__((always_inline)) {
         constexpr int COPIES = decltype(copies)::value;
-        constexpr int M = ACT * NT, R = P::kReads, C = P::kPer, H = M / (2 * C), W = P::kWords;
+        constexpr int M = ACT * NT, R = P::kReads, H = M / (2 * C);
         const auto half = p.place(st, step, 1), next = p.place(nx, step + 1, 0);
-        if (P::kTable && COPIES != kLast) p.look_up(step + 2);
+        if (P::kTable && COPIES != kLast) p.look_up(step + 3);
         const bool more = COPIES != kLast || step + 1 < steps;
         each([&](auto at) __attribute__((always_inline)) {  // (as a loop it is too much for the compiler to unroll)
             constexpr int m = decltype(at)::value;
@@ -408,13 +414,15 @@ __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int 
             p.mfma(h0, m / NT, m % NT, acc[m / NT][m % NT]);
             if (more) {
 #pragma unroll
-                for (int w = m * W / M; w < (m + 1) * W / M; ++w) p.put(nx, w);
+                for (int c = m * W / M; c < (m + 1) * W / M; ++c) {
+                    p.put(nx, c);
+                    if (COPIES != kLast && c % 16 == 15) p.template fetch<COPIES == kWhole>(step + 2, c / 16);
+                }
             }
             if (m % 2) pin();
         }, std::make_integer_sequence<int, M>());
-        wait_copies<0>();
-        if (COPIES != kLast) p.template fetch<COPIES == kWhole>(step + 2);
-        pin();
+        // the copies: this half's loads may be on their way. (A test counts them in the compiled kernels)
+        wait_copies<(COPIES == kLast ? 0 : 2 * P::kChunks)>();
         each([&](auto at) __attribute__((always_inline)) {
             constexpr int m = decltype(at)::value;
 #pragma unroll
@@ -956,13 +964,15 @@ struct WgradArgs {
 // tile. Rows of regions are looked up once a step, into LDS.
 template <bool KEPT, int CHUNKS>
 struct KeptRows {};
-// the scales, a lane's places in them and in the tile, what it has loaded and widened, the looked-up rows' place in LDS
+// the scales, a lane's place in them, its first chunk's in the tile, where the looked-up rows are, what it has loaded and widened
 template <int CHUNKS>
 struct KeptRows<true, CHUNKS> {
     const uint8_t *sb;
-    uint32_t so[CHUNKS], to[CHUNKS], table;
+    uint32_t so, to, table;
     u32x4 codes[CHUNKS], wide;
     uint8_t scale[CHUNKS];
+    uint32_t even;
+    float unit;
 };
 template <int BM, int BN, int WM, int WN, bool REGIONS, bool KEPT>
 struct Wgrad {
@@ -971,7 +981,8 @@ struct Wgrad {
     static constexpr int kGBytes = 64 * BM * 2, kXBytes = 64 * BN * 2, kStage = kGBytes + kXBytes, kStages = 2;
     static constexpr int kGPer = kGBytes / 1024 / kWaves, kXPer = kXBytes / 1024 / kWaves, kPer = kGPer + (KEPT ? 0 : kXPer);
     static constexpr int kSoon = kPer;
-    static constexpr int kChunks = kXBytes / 32 / kThreads, kWords = kChunks * 4;  // of 16 codes, and of 4, a lane's
+    static constexpr int kChunks = kXBytes / 32 / kThreads;  // of 16 codes, a lane's
+    static constexpr int kApart = kThreads / (BN / 16);      // rows between them
     static constexpr bool kTable = KEPT && REGIONS;
     static_assert(kGPer * kWaves * 1024 == kGBytes && kXPer * kWaves * 1024 == kXBytes, "whole copies per wave");
     using Frags = HalfFrags<ACT, NT, false>;
@@ -983,13 +994,13 @@ struct Wgrad {
     };
     struct Table {
         uint8_t ring[kStages * kStage];
-        int rows[128];  // receive rows of two steps
+        int rows[256];  // receive rows of four steps
     };
     using Shared = std::conditional_t<kTable, Table, Plain>;
 
     const GroupArgs *g;
     const uint8_t *gb, *xb;  // bases: packed layout, the expert's first row; low-latency, the arrays
-    uint32_t go[kGPer], xo[KEPT ? kChunks : kXPer];
+    uint32_t go[kGPer], xo[KEPT ? 1 : kXPer];
     int e, count, wave, lane, grow, xrow;  // rows' bytes
     KeptRows<KEPT, kChunks> kept;
 
@@ -1006,15 +1017,13 @@ struct Wgrad {
             go[i] = (uint32_t)r * grow + min(c, a.N - 8 - n0) * 2;
         }
         if constexpr (KEPT) {
+            // a lane's chunks: the same columns of every kApart-th row
+            const int at = wave * 64 + lane, r = at / (BN / 16), u = at % (BN / 16);
+            const int c = min(u * 16, a.K - 16 - k0);
             kept.sb = uniform(a.x_scales + base * (a.K / 32) + k0 / 32);
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int at = i * kThreads + wave * 64 + lane, r = at / (BN / 16), u = at % (BN / 16);
-                const int c = min(u * 16, a.K - 16 - k0);
-                xo[i] = (REGIONS ? 0 : (uint32_t)r * xrow) + c;
-                kept.so[i] = (REGIONS ? 0 : (uint32_t)r * (xrow / 32)) + c / 32;
-                kept.to[i] = kGBytes + r * (BN * 2) + ((u ^ tr_swizzle(r)) << 5);
-            }
+            kept.so = (REGIONS ? 0 : (uint32_t)r * (xrow / 32)) + c / 32;
+            xo[0] = (REGIONS ? 0 : (uint32_t)r * xrow) + c;
+            kept.to = kGBytes + r * (BN * 2) + ((u ^ tr_swizzle(r)) << 5);
         } else {
 #pragma unroll
             for (int i = 0; i < kXPer; ++i) {
@@ -1030,41 +1039,39 @@ struct Wgrad {
         if (wave == 0) {
             const int m = step * 64 + lane;
             const int row = m < count ? (int)ep::group_row(*g, e, m) : 0;
-            *(__attribute__((address_space(3))) int *)(uintptr_t)(kept.table + ((step & 1) * 64 + lane) * 4) = row;
+            *(__attribute__((address_space(3))) int *)(uintptr_t)(kept.table + ((step & 3) * 64 + lane) * 4) = row;
         }
     }
     __device__ __forceinline__ int64_t looked_up(int step, int r) const {
-        return lds_read<int>(kept.table + ((step & 1) * 64 + r) * 4);
+        return lds_read<int>(kept.table + ((step & 3) * 64 + r) * 4);
     }
 
-    // Load a step's codes and scales; WHOLE: all 64 rows are the expert's (others: zeros).
+    // Load chunk i of a step's codes and its scale; WHOLE: all 64 rows are the expert's (others: zeros).
     template <bool WHOLE>
-    __device__ __forceinline__ void fetch(int step) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int r = (i * kThreads + wave * 64 + lane) / (BN / 16);
-            int64_t row = (int64_t)step * 64;
-            if constexpr (REGIONS) row = looked_up(step, r);
-            const uint8_t *q = xb + row * xrow + xo[i], *s = kept.sb + row * (xrow / 32) + kept.so[i];
-            if (!WHOLE && step * 64 + r >= count) q = s = (const uint8_t *)&k_zero_chunk;
-            kept.codes[i] = *(const u32x4 *)q;
-            kept.scale[i] = *s;
+    __device__ __forceinline__ void fetch(int step, int i) {
+        const int r = (i * kThreads + wave * 64 + lane) / (BN / 16);
+        int64_t row = (int64_t)step * 64 + i * kApart;
+        if constexpr (REGIONS) row = looked_up(step, r);
+        const uint8_t *q = xb + row * xrow + xo[0], *s = kept.sb + row * (xrow / 32) + kept.so;
+        if (!WHOLE && step * 64 + r >= count) q = s = (const uint8_t *)&k_zero_chunk;
+        kept.codes[i] = *(const __attribute__((address_space(1))) u32x4 *)(uintptr_t)q;
+        kept.scale[i] = *(const __attribute__((address_space(1))) uint8_t *)(uintptr_t)s;
+    }
+    // Widen the lane's code c, and write eight of them when they are done.
+    __device__ __forceinline__ void put(uint32_t stage, int c) {
+        const int i = c / 16, k = c % 16;
+        if (k == 0) {  // 2^(b-133), what a code of 1 stands for
+            const int b = kept.scale[i];
+            kept.unit = b == 255 ? __builtin_nanf("") : ldexpf(1.0f, b - 133);
         }
+        const uint32_t f = __float_as_uint((float)((int)(kept.codes[i][k / 4] << (24 - 8 * (k % 4))) >> 24) * kept.unit);
+        if (k % 2)  // (the upper halves: they are bf16 numbers)
+            kept.wide[k % 8 / 2] = __builtin_amdgcn_perm(f, kept.even, 0x07060302);
+        else
+            kept.even = f;
+        if (k % 8 == 7)
+            *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(stage + kept.to + i * (kApart * BN * 2) + k / 8 * 16) = kept.wide;
     }
-    // Widen word w of the lane's codes, and write eight of them when they are done.
-    __device__ __forceinline__ void put(uint32_t stage, int w) {
-        const int i = w / 4;
-        const uint32_t word = kept.codes[i][w % 4], b = kept.scale[i];
-        const float unit = b == 255 ? __builtin_nanf("") : __uint_as_float(b > 6 ? (b - 6) << 23 : 1u << (16 + b));  // 2^(b-133)
-        uint32_t f[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = __float_as_uint((float)((int)(word << (24 - 8 * c)) >> 24) * unit);
-        kept.wide[w % 2 * 2] = (f[1] & 0xFFFF0000u) | f[0] >> 16;
-        kept.wide[w % 2 * 2 + 1] = (f[3] & 0xFFFF0000u) | f[2] >> 16;
-        if (w % 2)
-            *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(stage + kept.to[i] + w % 4 / 2 * 16) = kept.wide;
-    }
-
     template <bool WHOLE>
     __device__ __forceinline__ void copy(int step, uint32_t stage, int c) const {
         const bool of_grad = c < kGPer;
@@ -1126,6 +1133,7 @@ struct Wgrad {
             if (count > 0) {
                 __syncthreads();  // the last tile's reads of the ring are done
                 if constexpr (KEPT) {
+                    static_assert(kApart % 16 == 0, "the tile's swizzle");
                     Wgrad w(a, e, count, n0, k0, wave, lane);
                     if constexpr (kTable) w.kept.table = lds_address(sh.rows);
                     reduce_kept(w, lds_address(sh.ring), (count + 63) / 64, REGIONS ? 0 : count / 64, acc);

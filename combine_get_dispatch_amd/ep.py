@@ -1143,13 +1143,12 @@ class Router:
     group_top: int = 2
 
     def c(self) -> EpRouter:
+        E, k, G, kept, top = self.num_experts, self.num_topk, self.num_groups, self.topk_groups, self.group_top
         if self.score not in _SCORES:
             raise EpError(EP_ERR_ARG, f"score {self.score!r} is neither softmax nor sigmoid")
-        sizes = (self.num_experts, self.num_topk, self.num_groups, self.topk_groups, self.group_top)
-        if any(s >> 31 for s in sizes):
-            _not_c_ints(*sizes)
-        return EpRouter(self.num_experts, self.num_topk, _SCORES[self.score], int(bool(self.renormalize)),
-                        self.num_groups, self.topk_groups, self.group_top, self.scale)
+        if (E | k | G | kept | top) >> 31:
+            _not_c_ints(E, k, G, kept, top)
+        return EpRouter(E, k, _SCORES[self.score], 1 if self.renormalize else 0, G, kept, top, self.scale)
 
 
 def _logits(logits, router: Router, dev: int):
@@ -1170,8 +1169,7 @@ def route(logits, router: Router, bias=None, out=None):
     b = None if bias is None else _tensor(bias, "bias", _torch.float32, (router.num_experts,), dev)
     shape = (T, router.num_topk)
     if out is None:
-        out = (_torch.empty(shape, dtype=_torch.int32, device=logits.device),
-               _torch.empty(shape, dtype=_torch.float32, device=logits.device))
+        out = logits.new_empty(shape, dtype=_torch.int32), logits.new_empty(shape, dtype=_torch.float32)
     idx, w = out
     ep_route(r, p, logits.dtype is _torch.float32, b, T, _tensor(idx, "topk_idx", _torch.int32, shape, dev),
              _tensor(w, "topk_weights", _torch.float32, shape, dev), _raw_stream(dev))
