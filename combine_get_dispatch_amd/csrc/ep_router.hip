@@ -31,9 +31,10 @@ struct RouteArgs {
     int32_t *idx;
     float *w;
     int T, E, k, G, kept, top;
-    int gs, lg;      // experts and lanes per group
+    int gs, lg, lg_log;  // experts and lanes per group, and the lanes' logarithm
     int exact;       // c_e is a score in 64 bits, else the logit
-    int sigmoid, renorm, vector;
+    int sigmoid, renorm;
+    int vector, quads;  // logits come in vectors; a lane's experts start at a multiple of four
     float scale;
 };
 
@@ -259,6 +260,59 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t at, float (&l
 // route
 // ---------------------------------------------------------------------------
 
+// Whether a lane's group stays, one and two its two largest numbers (with indices), in all its lanes.
+template <int L>
+__device__ __forceinline__ bool group_kept(const RouteArgs &a, double one, double two, float top, int group) {
+    double value = value_of(one);
+    if (a.top == 2) {
+        const double second = value_of(two);
+        if (a.exact) {
+            value += two > minus_inf() ? second : 0.0;
+        } else {  // the scores of the two logits (softmax's without its sum)
+            auto score = [&](double l) __attribute__((always_inline)) {
+                const float x = (float)l;  // (the largest numbers stand for infinity)
+                return a.sigmoid ? sigmoid64(x) : x == top ? 1.0 : exp64((double)x - (double)top);
+            };
+            value = one > minus_inf() ? score(value) + (two > minus_inf() ? score(second) : 0.0) : minus_inf();
+        }
+    }
+    int ahead = 0;
+    for (int g = 0; g < a.G; ++g) {
+        const double other = __shfl(value, g * a.lg, L);
+        ahead += other > value || (other == value && g < group);
+    }
+    return ahead < a.kept;
+}
+
+// Weights of the chosen experts (open: this lane has one, of logit x): divided by their sum, or of all scores' (total, over
+// top's exponential, for softmax).
+template <int L>
+__device__ __forceinline__ float weight_of(const RouteArgs &a, bool open, float x, float top, float total) {
+    float w;
+    if (a.renorm) {  // over the largest of the chosen logits, so that none underflows all
+        const float y = a.sigmoid ? fminf(x, 0.0f) : x;
+        const float m = all<L>(open ? y : -INFINITY, Max());
+        w = open ? exp32(y == m ? 0.0f : y - m) : 0.0f;
+        if (a.sigmoid && open) w /= sigmoid_den(x);
+        const float sum = all<L>(w, Sum());
+        w = w / sum * a.scale;
+    } else if (a.sigmoid) {
+        w = exp32(fminf(x, 0.0f)) / sigmoid_den(x) * a.scale;
+    } else {
+        w = exp32(x == top ? 0.0f : x - top) / total * a.scale;
+    }
+    return open ? w : 0.0f;
+}
+
+// softmax's sum over a token's experts, over the exponential of their largest logit
+template <int L, int P>
+__device__ __forceinline__ float sum_of(const float (&l)[P], int mine, float top) {
+    float total = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) total += p < mine ? exp32(l[p] == top ? 0.0f : l[p] - top) : 0.0f;
+    return all<L>(total, Sum());
+}
+
 template <int L, int P, bool BF16>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
     const int lane = threadIdx.x & 63, sub = lane % L;
@@ -298,12 +352,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
         if (!a.exact) {
 #pragma unroll
             for (int p = 0; p < P; ++p) v[p] = l[p];
-            if (sums) {
-                total = 0.0f;
-#pragma unroll
-                for (int p = 0; p < P; ++p) total += p < mine ? exp32(l[p] == top ? 0.0f : l[p] - top) : 0.0f;
-                total = all<L>(total, Sum());
-            }
+            if (sums) total = sum_of<L>(l, mine, top);
         } else if (a.sigmoid) {
 #pragma unroll
             for (int p = 0; p < P; ++p) v[p] = sigmoid64(l[p]) + (double)bias[p];
@@ -345,25 +394,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
                 if (a.lg > 16) merge(std::integral_constant<int, 4>());
                 if (a.lg > 32) merge(std::integral_constant<int, 5>());
             }
-            double value = value_of(one);
-            if (a.top == 2) {
-                const double second = value_of(two);
-                if (a.exact) {
-                    value += two > minus_inf() ? second : 0.0;
-                } else {  // the scores of the two logits (softmax's without its sum)
-                    auto score = [&](double l) __attribute__((always_inline)) {
-                        const float x = (float)l;  // (the largest numbers stand for infinity)
-                        return a.sigmoid ? sigmoid64(x) : x == top ? 1.0 : exp64((double)x - (double)top);
-                    };
-                    value = one > minus_inf() ? score(value) + (two > minus_inf() ? score(second) : 0.0) : minus_inf();
-                }
-            }
-            int ahead = 0;
-            for (int g = 0; g < a.G; ++g) {
-                const double other = __shfl(value, g * a.lg, L);
-                ahead += other > value || (other == value && g < group);
-            }
-            if (ahead >= a.kept) {
+            if (!group_kept<L>(a, one, two, top, group)) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) v[p] = minus_inf();
             }
@@ -373,24 +404,245 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a) {
         const bool open = sub < a.k && won > minus_inf();
         const int e = open ? index_of(won) : 0;
         const float x = open ? load_logit<BF16>(a.logits, row + e) : -INFINITY;
-        float w;
-        if (a.renorm) {  // over the largest of the chosen logits, so that none underflows all
-            const float y = a.sigmoid ? fminf(x, 0.0f) : x;
-            const float m = all<L>(y, Max());
-            w = open ? exp32(y == m ? 0.0f : y - m) : 0.0f;
-            if (a.sigmoid && open) w /= sigmoid_den(x);
-            const float sum = all<L>(w, Sum());
-            w = open ? w / sum * a.scale : 0.0f;
-        } else if (a.sigmoid) {
-            w = open ? exp32(fminf(x, 0.0f)) / sigmoid_den(x) * a.scale : 0.0f;
-        } else {
-            w = open ? exp32(x == top ? 0.0f : x - top) / total * a.scale : 0.0f;
-        }
+        float w = weight_of<L>(a, open, x, top, total);
         if (poisoned) w = __builtin_nanf("");
         if (on && sub < a.k) {
             a.idx[token * a.k + sub] = open ? e : -1;
             a.w[token * a.k + sub] = w;
         }
+    }
+}
+
+// Numbers that are compared as integers as floats are: the largest of a token's
+// lanes is then one instruction a step.
+__device__ __forceinline__ int ordered(float f) {
+    const int b = __float_as_int(f);
+    return b ^ (b >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float of_ordered(int b) { return __int_as_float(b ^ (b >> 31 & 0x7FFFFFFF)); }
+template <int CTRL>
+__device__ __forceinline__ int lane_max(int v) {
+    return max(v, (int)from_lane<CTRL>((uint32_t)v));
+}
+__device__ __forceinline__ int max16(int v) {
+    return lane_max<0x140>(lane_max<0x141>(lane_max<0x4E>(lane_max<0xB1>(v))));
+}
+
+// 16 lanes' numbers in falling order: of sorted runs of 1, 2, 4 and 8 lanes the
+// larger halves against the other run's mirror image, then within the halves.
+template <int CTRL>
+__device__ __forceinline__ double other(double v) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(double, (u32x2{from_lane<CTRL>(w.x), from_lane<CTRL>(w.y)}));
+}
+__device__ __forceinline__ double pick(double a, double b, bool larger) {
+    const double most = __builtin_fmax(a, b), least = __builtin_fmin(a, b);
+    return larger ? most : least;
+}
+__device__ __forceinline__ double sort16(double v, int sub) {
+    constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror4 = 0x1B, kMirror8 = 0x141, kMirror16 = 0x140;
+    const bool b0 = !(sub & 1), b1 = !(sub & 2), b2 = !(sub & 4), b3 = !(sub & 8);
+    v = pick(v, other<kXor1>(v), b0);
+    v = pick(v, other<kMirror4>(v), b1);
+    v = pick(v, other<kXor1>(v), b0);
+    v = pick(v, other<kMirror8>(v), b2);
+    v = pick(v, other<kXor2>(v), b1);
+    v = pick(v, other<kXor1>(v), b0);
+    v = pick(v, other<kMirror16>(v), b3);
+    v = pick(v, other<kMirror8>(other<kMirror4>(v)), b2);  // four lanes away
+    v = pick(v, other<kXor2>(v), b1);
+    return pick(v, other<kXor1>(v), b0);
+}
+
+// The same for many tokens: 16 lanes a token, k <= 8 of at most 256 experts, no
+// bias with softmax. 64-bit numbers only for candidates: by c_e in 32 bits, off
+// by little, every lane finds its two largest, the k-th largest of all lanes' two
+// bounds the k-th largest of all from below, and what may reach it, some 8 to 12
+// experts (more where many logits are equal), goes to a lane each, 16 at a time,
+// to be ordered by the exact numbers. Groups are ordered by 32 bits where those
+// decide, else exactly.
+__host__ __device__ constexpr int place(int e) { return e + e / 16 * 4; }
+
+template <int P, bool BF16>
+__global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
+    constexpr int L = 16, kTokens = 256 / L, kRow = L * P, kVec = BF16 ? 8 : 4;
+    constexpr float kMost = 3.402823466e38f;
+    // logits and biases, four words left out after 16: lanes that read 16 neighbours each then fall on different banks
+    __shared__ alignas(16) float rows[kTokens][place(kRow)], biases[place(kRow)];
+    __shared__ uint8_t found[kTokens][kRow];  // candidates
+    const int lane = threadIdx.x & 63, sub = lane % L, slot = threadIdx.x / L;
+    const int group = sub >> a.lg_log, first = (sub & (a.lg - 1)) * P, e0 = group * a.gs + first;
+    const int mine = group < a.G ? min(max(a.gs - first, 0), P) : 0;
+    const int64_t token = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const bool on = token < a.T;
+    const int64_t row = (on ? token : (int64_t)a.T - 1) * a.E;
+    // neighbouring lanes read neighbouring logits; by way of LDS every lane gets its own
+    if (a.vector) {
+        float v[P / kVec > 0 ? P / kVec : 1][kVec];
+#pragma unroll
+        for (int i = 0; i * kVec < P; ++i) {
+            const int e = (i * L + sub) * kVec;
+            if (e < a.E) load_logits<BF16, kVec>(a.logits, row + e, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i * kVec < P; ++i) {
+            const int e = (i * L + sub) * kVec;
+            if (e < a.E)
+#pragma unroll
+                for (int q = 0; q < kVec; q += 4) *(f32x4 *)&rows[slot][place(e + q)] = f32x4{v[i][q], v[i][q + 1], v[i][q + 2], v[i][q + 3]};
+        }
+    } else {
+        for (int e = sub; e < a.E; e += L) rows[slot][place(e)] = load_logit<BF16>(a.logits, row + e);
+    }
+    if (a.bias && (int)threadIdx.x < a.E) biases[place(threadIdx.x)] = a.bias[threadIdx.x];
+    __syncthreads();
+    float l[P], c[P];
+    if (P >= 4 && a.quads && mine == P) {
+#pragma unroll
+        for (int p = 0; p < P; p += 4) {
+            const f32x4 v = *(const f32x4 *)&rows[slot][place(e0 + p)];
+            const f32x4 b = a.bias ? *(const f32x4 *)&biases[place(e0 + p)] : f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (p + q < P) l[p + q] = v[q], c[p + q] = b[q];
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            l[p] = p < mine ? rows[slot][place(e0 + p)] : -INFINITY;
+            c[p] = a.bias && p < mine ? biases[place(e0 + p)] : 0.0f;
+        }
+    }
+    bool bad = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        bad |= l[p] != l[p];
+        top = fmaxf(top, l[p]);
+    }
+    const bool poisoned = (__ballot(bad) >> (lane & 48) & 0xFFFF) != 0;
+    top = of_ordered(max16(ordered(top)));
+    const float total = !a.sigmoid && !a.renorm ? sum_of<L>(l, mine, top) : 1.0f;
+    float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        // within 2^-22 of the score, and the sum's rounding (NaN: not open)
+        float v = l[p];
+        if (a.exact) v = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[p] * -1.44269504f)) + c[p];
+        c[p] = l[p] > -INFINITY && v > -INFINITY ? v : -INFINITY;
+        two = __builtin_amdgcn_fmed3f(one, two, c[p]);
+        one = __builtin_amdgcn_fmed3f(one, c[p], INFINITY);
+    }
+    // exact number of expert e, -infinity if it is not open
+    auto number = [&](int e, bool in) __attribute__((always_inline)) {
+        const float x = in ? rows[slot][place(e)] : -INFINITY;
+        double v = x;
+        if (a.exact) v = sigmoid64(x) + (double)biases[place(e)];
+        return x > -INFINITY && v > minus_inf() ? with_index(v, e) : minus_inf();
+    };
+    if (a.G > 1) {
+        float g1 = one, g2 = two;
+        auto merge = [&](auto s) __attribute__((always_inline)) {
+            constexpr int S = decltype(s)::value;
+            const float low = step<S>(g1, [](float x, float y) { return fminf(x, y); });
+            g2 = fmaxf(low, step<S>(g2, Max()));
+            g1 = step<S>(g1, Max());
+        };
+        if (a.lg > 1) merge(std::integral_constant<int, 0>());
+        if (a.lg > 2) merge(std::integral_constant<int, 1>());
+        if (a.lg > 4) merge(std::integral_constant<int, 2>());
+        // the group's value, and how far apart two have to be for 32 bits to tell: without a bias a largest logit is exact (but
+        // a tie is left to the exact form), and scores that underflow are never told apart
+        float value = g1, far = 0.0f;
+        if (a.exact) {
+            value = fminf(a.top == 2 && g2 > -INFINITY ? g1 + g2 : g1, kMost);
+            far = 0x1p-20f + 0x1p-21f * fabsf(value);
+        } else if (a.top == 2) {
+            auto score = [&](float x) __attribute__((always_inline)) {
+                if (a.sigmoid) return exp32(fminf(x, 0.0f)) / sigmoid_den(x);
+                return exp32(x == top ? 0.0f : x - top);
+            };
+            value = g1 > -INFINITY ? score(g1) + (g2 > -INFINITY ? score(g2) : 0.0f) : -INFINITY;
+            far = 0x1p-19f * value + 0x1p-100f;
+        }
+        const int mark = ordered(value);
+        int left = mark, last = 0;
+        for (int j = 0; j < a.kept; ++j) {
+            last = max16(left);
+            left = left == last ? ordered(-INFINITY) : left;
+        }
+        bool closed = mark < last;
+        // the first group that does not stay may be too near the last that does; equal ones were counted once
+        const float gap = of_ordered(last) - of_ordered(max16(left));
+        const bool in = !closed && value > -INFINITY;
+        const int stay = __popcll(__ballot(in && (sub & (a.lg - 1)) == 0) >> (lane & 48) & 0xFFFF);
+        const bool unsure = in && (stay > a.kept || (mark == last && gap <= far));
+        if (__builtin_expect(__ballot(unsure) != 0, 0)) {  // some group of the wave's tokens: all its groups exactly
+            double d1 = minus_inf(), d2 = minus_inf();
+#pragma unroll 1
+            for (int p = 0; p < P; ++p) {
+                const double v = number(p < mine ? e0 + p : 0, p < mine);
+                d2 = __builtin_fmax(d2, __builtin_fmin(d1, v));
+                d1 = __builtin_fmax(d1, v);
+            }
+            auto merge64 = [&](auto s) __attribute__((always_inline)) {
+                constexpr int S = decltype(s)::value;
+                const double low = step<S>(d1, [](double x, double y) { return __builtin_fmin(x, y); });
+                d2 = __builtin_fmax(low, step<S>(d2, Max()));
+                d1 = step<S>(d1, Max());
+            };
+            if (a.lg > 1) merge64(std::integral_constant<int, 0>());
+            if (a.lg > 2) merge64(std::integral_constant<int, 1>());
+            if (a.lg > 4) merge64(std::integral_constant<int, 2>());
+            closed = !group_kept<L>(a, d1, d2, top, group);
+        }
+        if (closed) {
+            one = two = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < P; ++p) c[p] = -INFINITY;
+        }
+    }
+    // the k-th largest of the lanes' two (equal ones counted once: lower still), and what it may be off
+    int mark = 0;
+    for (int j = 0, x = ordered(one), y = ordered(two); j < a.k; ++j) {
+        mark = max16(x);
+        const bool won = x == mark;
+        x = won ? y : x;
+        y = won ? ordered(-INFINITY) : y;
+    }
+    float least = fminf(fmaxf(of_ordered(mark), -kMost), kMost);
+    if (a.exact) least = fmaxf(least - (0x1p-20f + 0x1p-21f * fabsf(least)), -kMost);
+    uint32_t those = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) those |= c[p] >= least ? 1u << p : 0u;
+    const int n = __popc(those);
+    int before = n;  // candidates of the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) {
+        const int u = __shfl_up(before, d, L);
+        before += sub >= d ? u : 0;
+    }
+    const int many = __shfl(before, L - 1, L);
+    for (int i = before - n; those; ++i) {
+        found[slot][i] = (uint8_t)(e0 + __builtin_ctz(those));
+        those &= those - 1;
+    }
+    __builtin_amdgcn_wave_barrier();  // (a token's candidates are its wave's own)
+    double won = minus_inf();
+#pragma unroll 1
+    for (int from = 0; __ballot(from < many); from += L) {  // the 16 largest so far, the j-th in lane j, and 16 more
+        const bool in = from + sub < many;
+        const double v = sort16(number(in ? found[slot][from + sub] : 0, in), sub);
+        won = from == 0 ? v : sort16(__builtin_fmax(won, other<0x140>(v)), sub);
+    }
+    const bool open = sub < a.k && won > minus_inf();
+    const int e = open ? index_of(won) : 0;
+    const float x = open ? rows[slot][place(e)] : -INFINITY;
+    float w = weight_of<L>(a, open, x, top, total);
+    if (poisoned) w = __builtin_nanf("");
+    if (on && sub < a.k) {
+        a.idx[token * a.k + sub] = open ? e : -1;
+        a.w[token * a.k + sub] = w;
     }
 }
 
@@ -501,6 +753,16 @@ int bad_router(const ep_router *r) {
     return EP_OK;
 }
 
+template <int P>
+hipError_t launch_route_many(const RouteArgs &a, bool bf16, hipStream_t s) {
+    const int grid = (a.T + 15) / 16;
+    if (bf16)
+        k_route_many<P, true><<<grid, 256, 0, s>>>(a);
+    else
+        k_route_many<P, false><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int L, int P>
 hipError_t launch_route(const RouteArgs &a, bool bf16, int cus, hipStream_t s) {
     const int64_t waves = ((int64_t)a.T * L + 63) / 64;
@@ -555,12 +817,25 @@ int ep_route(const ep_router *router, const void *logits, int logits_f32, const 
     const bool narrow = all <= 16 && a.k <= 16 && (int64_t)(a.gs + 16 / all - 1) / (16 / all) <= 16 && T >= 16 * (int64_t)cus;
     const int L = narrow ? 16 : 64;
     a.lg = L / all;
+    a.lg_log = __builtin_ctz(a.lg);
     const int P = power_of_two((a.gs + a.lg - 1) / a.lg);
+    a.quads = 0;
     a.vector = a.gs % P == 0 && !misaligned(logits, 16);  // P experts at a multiple of their size
     const hipStream_t s = (hipStream_t)stream;
     const bool bf16 = !logits_f32;
     hipError_t e;
-    if (narrow)
+    const bool many = narrow && a.k <= 8 && (a.sigmoid || !a.exact);
+    if (many) {
+        a.vector = a.E % (bf16 ? 8 : 4) == 0 && P >= (bf16 ? 8 : 4) && !misaligned(logits, 16);
+        a.quads = P >= 4 && a.gs % 4 == 0;
+    }
+    if (many)
+        e = P == 1   ? launch_route_many<1>(a, bf16, s)
+            : P == 2 ? launch_route_many<2>(a, bf16, s)
+            : P == 4 ? launch_route_many<4>(a, bf16, s)
+            : P == 8 ? launch_route_many<8>(a, bf16, s)
+                     : launch_route_many<16>(a, bf16, s);
+    else if (narrow)
         e = P == 1   ? launch_route<16, 1>(a, bf16, cus, s)
             : P == 2 ? launch_route<16, 2>(a, bf16, cus, s)
             : P == 4 ? launch_route<16, 4>(a, bf16, cus, s)
