@@ -29,6 +29,7 @@ using ep::GroupArgs;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
@@ -146,24 +147,37 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&f)[8], uint8_t &scal
     return bad ? 0 : v;
 }
 
-// Eight MXINT8 codes of a lane and the scale byte of its four lanes' group.
-__device__ __forceinline__ u32x2 mx8_codes(const float (&f)[8], uint8_t &scale) {
-    uint32_t top = 0;
+// Four whole numbers as bytes: of magnitudes up to 127, each added to 1.5 * 2^23,
+// whose sum has the nearest whole number (ties to even) in its low bits.
+constexpr float kWhole = 12582912.0f;
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+    const uint32_t ab = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0C0C0400);
+    const uint32_t cd = __builtin_amdgcn_perm(__float_as_uint(d), __float_as_uint(c), 0x04000C0C);
+    return ab | cd;
+}
+
+// MXINT8 codes of a lane's eight bf16 values and the scale byte of its four lanes' group.
+__device__ __forceinline__ u32x2 mx8_codes(u32x4 w, uint8_t &scale) {
+    u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int k = 0; k < 4; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[k] & 0x7FFF7FFFu));
+    uint32_t top = max(m.x, m.y);
     top = max(top, from_lane<0xB1>(top));
     top = max(top, from_lane<0x4E>(top));
-    const int field = (int)(top >> 23);  // as in mx4_codes; a bf16 subnormal's group: 0, which is 2^-127
+    const int field = (int)(top >> 7);  // as in mx4_codes; a subnormal's group: 0, which is 2^-127
     const bool bad = field == 255;
     scale = (uint8_t)field;
-    // x / 2^(field - 133), exact: bf16 values have 8 bits. A half of the power twice (each of them a normal number)
-    const int up = 133 - field;
-    const float a = __uint_as_float((uint32_t)(127 + up / 2) << 23), b = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
-    uint32_t q[2] = {0, 0};
+    uint32_t q[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = fminf(fmaxf(__builtin_rintf(f[i] * a * b), -127.0f), 127.0f);
-        q[i / 4] |= ((uint32_t)(int)r & 0xFF) << (8 * (i % 4));
+    for (int i = 0; i < 2; ++i) {
+        float z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // x / 2^(field - 133), exact
+            const uint32_t u = w[2 * i + k / 2];
+            const float y = __builtin_amdgcn_ldexpf(k % 2 ? hi16(u) : lo16(u), 133 - field);
+            z[k] = __builtin_amdgcn_fmed3f(y, -127.0f, 127.0f) + kWhole;
+        }
+        q[i] = low_bytes(z[0], z[1], z[2], z[3]);
     }
     return bad ? u32x2{0, 0} : u32x2{q[0], q[1]};
 }
@@ -221,43 +235,25 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
             o[k] = pack_bf16(f[0], f[1]);
         }
         store(o, (uint16_t *)a.out + at);
-    } else if constexpr (OP == kDequantizeMx8) {
-        const float unit = mx8_unit(v[0].z);
-        u32x4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = pack_bf16(mx8_code(v[0][k / 2], k % 2 * 2) * unit, mx8_code(v[0][k / 2], k % 2 * 2 + 1) * unit);
-        store(o, (uint16_t *)a.out + at);
-    } else if constexpr (OP == kSwigluGrad || OP == kSwigluKeptGrad) {
-        u32x4 og, ou, oh;
-        float unit[2];
-        if constexpr (OP == kSwigluKeptGrad) unit[0] = mx8_unit(v[0].z), unit[1] = mx8_unit(v[1].z);
+    } else if constexpr (OP == kSwigluGrad) {
+        u32x4 og, ou;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            float dg[2], du[2], y[2];
+            float dg[2], du[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float g, u;
-                if constexpr (OP == kSwigluKeptGrad) {
-                    g = mx8_code(v[0][k / 2], k % 2 * 2 + h) * unit[0];
-                    u = mx8_code(v[1][k / 2], k % 2 * 2 + h) * unit[1];
-                } else {
-                    g = h ? hi16(v[0][k]) : lo16(v[0][k]), u = h ? hi16(v[1][k]) : lo16(v[1][k]);
-                }
+                const float g = h ? hi16(v[0][k]) : lo16(v[0][k]), u = h ? hi16(v[1][k]) : lo16(v[1][k]);
                 const float d = h ? hi16(v[2][k]) : lo16(v[2][k]);
                 const float s = sigmoid(g), gs = g * s;
                 dg[h] = d * u * fmaf(gs, 1.0f - s, s);
                 du[h] = d * gs;
-                y[h] = gs * u;
             }
             og[k] = pack_bf16(dg[0], dg[1]);
             ou[k] = pack_bf16(du[0], du[1]);
-            oh[k] = pack_bf16(y[0], y[1]);
         }
         uint16_t *o = (uint16_t *)a.out + row * 2 * a.cols + c;
         store(og, o);
         store(ou, o + a.cols);
-        if (OP == kSwigluKeptGrad && a.again) store(oh, a.again + at);
     } else {
         float f[8];
 #pragma unroll
@@ -265,28 +261,12 @@ __device__ __forceinline__ void write_lane(const RowsArgs &a, int64_t row, int64
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float g = h ? hi16(v[0][k]) : lo16(v[0][k]);
-                if constexpr (OP == kQuantize || OP == kQuantizeMx8)
+                if constexpr (OP == kQuantize)
                     f[2 * k + h] = g;
                 else
                     f[2 * k + h] = g * sigmoid(g) * (h ? hi16(v[1][k]) : lo16(v[1][k]));
             }
-        if constexpr (OP == kSwigluKeep) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // gate, up
-                float x[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[2 * k] = lo16(v[i][k]), x[2 * k + 1] = hi16(v[i][k]);
-                const int64_t to = row * 2 * a.cols + i * a.cols + c;
-                uint8_t s;
-                store(mx8_codes(x, s), a.keep + to);
-                if ((threadIdx.x & 3) == 0) ((uint8_t *)a.scales)[to / 32] = s;
-            }
-        }
-        if constexpr (OP == kQuantizeMx8) {
-            uint8_t s;
-            store(mx8_codes(f, s), (uint8_t *)a.out + at);
-            if ((threadIdx.x & 3) == 0) ((uint8_t *)a.scales)[at / 32] = s;
-        } else if constexpr (OP == kSwigluBf16 || OP == kSwigluKeep) {
+        if constexpr (OP == kSwigluBf16) {
             store(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])},
                   (uint16_t *)a.out + at);
         } else if constexpr (OP == kSwigluMx4 || OP == kQuantize) {
@@ -373,6 +353,138 @@ hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) 
 }
 
 // ---------------------------------------------------------------------------
+// 8-bit checkpoints
+// ---------------------------------------------------------------------------
+
+// what a lane makes of its eight channels: bf16 results, codes and scales
+struct Made {
+    u32x4 wide[3];
+    u32x2 codes[2];
+    uint8_t scale[2];
+};
+
+template <int OP>
+__device__ __forceinline__ void make(const u32x4 *v, Made &m) {
+    if constexpr (OP == kQuantizeMx8) {
+        m.codes[0] = mx8_codes(v[0], m.scale[0]);
+    } else if constexpr (OP == kDequantizeMx8) {
+        const float unit = mx8_unit(v[0].z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            m.wide[0][k] =
+                pack_bf16(mx8_code(v[0][k / 2], k % 2 * 2) * unit, mx8_code(v[0][k / 2], k % 2 * 2 + 1) * unit);
+    } else if constexpr (OP == kSwigluKeep) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m.codes[i] = mx8_codes(v[i], m.scale[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float g = h ? hi16(v[0][k]) : lo16(v[0][k]);
+                f[h] = g * sigmoid(g) * (h ? hi16(v[1][k]) : lo16(v[1][k]));
+            }
+            m.wide[0][k] = pack_bf16(f[0], f[1]);
+        }
+    } else {
+        const float gate = mx8_unit(v[0].z), up = mx8_unit(v[1].z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float dg[2], du[2], y[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float g = mx8_code(v[0][k / 2], k % 2 * 2 + h) * gate;
+                const float u = mx8_code(v[1][k / 2], k % 2 * 2 + h) * up;
+                const float d = h ? hi16(v[2][k]) : lo16(v[2][k]);
+                const float s = sigmoid(g), gs = g * s;
+                dg[h] = d * u * fmaf(gs, 1.0f - s, s);
+                du[h] = d * gs;
+                y[h] = gs * u;
+            }
+            m.wide[0][k] = pack_bf16(dg[0], dg[1]);
+            m.wide[1][k] = pack_bf16(du[0], du[1]);
+            m.wide[2][k] = pack_bf16(y[0], y[1]);
+        }
+    }
+}
+
+template <int OP>
+__device__ __forceinline__ void write_made(const RowsArgs &a, int64_t row, int64_t c, const Made &m) {
+    const int64_t at = row * a.cols + c;
+    if constexpr (OP == kQuantizeMx8) {
+        store(m.codes[0], (uint8_t *)a.out + at);
+    } else if constexpr (OP == kDequantizeMx8) {
+        store(m.wide[0], (uint16_t *)a.out + at);
+    } else if constexpr (OP == kSwigluKeep) {
+        store(m.wide[0], (uint16_t *)a.out + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) store(m.codes[i], a.keep + row * 2 * a.cols + i * a.cols + c);  // gate, up
+    } else {
+        uint16_t *o = (uint16_t *)a.out + row * 2 * a.cols + c;
+        store(m.wide[0], o);
+        store(m.wide[1], o + a.cols);
+        if (a.again) store(m.wide[2], a.again + at);
+    }
+}
+
+template <int OP>
+__device__ __forceinline__ void write_scales(const RowsArgs &a, int64_t row, int64_t c, const Made &m) {
+    if constexpr (OP == kQuantizeMx8) {
+        ((uint8_t *)a.scales)[(row * a.cols + c) / 32] = m.scale[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ((uint8_t *)a.scales)[(row * 2 * a.cols + i * a.cols + c) / 32] = m.scale[i];
+    }
+}
+
+// A wave takes segments of up to C chunks of a row: all their loads, then all
+// results, then all stores, the single scale bytes last. (Stores between a
+// wave's loads cost more than what they overlap with: quantization of 32768 rows
+// x 7168, whole rows either way, 147 us in place of 116; SwiGLU that keeps its
+// input, 65536 rows x 2048, 200 us chunk by chunk and 179 by fours.) On MI355X,
+// memory bounds all four: that quantization 113 us (6.3 TB/s), of 16384 rows 55.5
+// and back 56.6 us (6.4 and 6.3), SwiGLU that keeps 179 us (6.0), its gradient with
+// the forward result 218 us (6.2; 232 with a fourth of the workgroups).
+template <int OP, int C>
+__global__ __launch_bounds__(kThreads) void k_segments(RowsArgs a) {
+    __shared__ int ends[ep::kGroupsMaxExperts];
+    const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * (kThreads / 64);
+    const int64_t segments = (a.cols + 512 * C - 1) / (512 * C), items = rows * segments;
+    RowWalk walk{&a.g, ends, 0, 0, 0, 0};
+    for (int64_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)); item < items;
+         item += waves) {
+        const int64_t entry = segments == 1 ? item : item / segments;
+        const int64_t row = a.grouped ? walk.row((int)entry) : entry;
+        const int64_t c = (item - entry * segments) * 512 * C + lane * kPer;
+        u32x4 v[C][kVecs<OP>];
+        Made m[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) load_lane<OP>(a, row, c + i * 512 < a.cols ? c + i * 512 : 0, v[i]);  // past the end: any
+#pragma unroll
+        for (int i = 0; i < C; ++i) make<OP>(v[i], m[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (c + i * 512 < a.cols) write_made<OP>(a, row, c + i * 512, m[i]);
+        if constexpr (OP == kQuantizeMx8 || OP == kSwigluKeep) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (c + i * 512 < a.cols && (lane & 3) == 0) write_scales<OP>(a, row, c + i * 512, m[i]);
+        }
+    }
+}
+
+template <int OP, int C>
+hipError_t launch_segments(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
+    const int64_t items = rows * ((a.cols + 512 * C - 1) / (512 * C)), blocks = (items + kThreads / 64 - 1) / (kThreads / 64);
+    const int64_t most = (int64_t)cus * (OP == kSwigluKeptGrad ? 256 : 64);
+    k_segments<OP, C><<<(int)(blocks < 1 ? 1 : blocks < most ? blocks : most), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // 8-bit integers with one scale per row
 // ---------------------------------------------------------------------------
 
@@ -380,7 +492,7 @@ hipError_t launch_rows(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) 
 // is read twice, C = 0): the scale needs the largest of all. SWIGLU: of
 // silu(gate) up in place of the values.
 template <int C, bool SWIGLU>
-__global__ __launch_bounds__(kThreads) void k_row_int8(RowsArgs a) {
+__global__ __launch_bounds__(kThreads, C >= 16 ? 3 : 1) void k_row_int8(RowsArgs a) {
     __shared__ int ends[ep::kGroupsMaxExperts];
     const int64_t rows = a.grouped ? ep::group_scan(a.g, ends, kThreads) : a.num_rows;
     const int lane = threadIdx.x & 63;
@@ -419,27 +531,28 @@ __global__ __launch_bounds__(kThreads) void k_row_int8(RowsArgs a) {
         };
         auto write = [&](int i, const float (&f)[8], float inv, bool bad) __attribute__((always_inline)) {
             const int c = i * 512 + lane * 8;
-            uint32_t q[2] = {0, 0};
+            uint32_t q[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                q[k / 4] |= ((uint32_t)(int)__builtin_rintf(f[k] * inv) & 0xFF) << (8 * (k % 4));
+            for (int k = 0; k < 2; ++k)
+                q[k] = low_bytes(f[4 * k] * inv + kWhole, f[4 * k + 1] * inv + kWhole, f[4 * k + 2] * inv + kWhole,
+                                 f[4 * k + 3] * inv + kWhole);
             if (c < a.cols) store(bad ? u32x2{0, 0} : u32x2{q[0], q[1]}, (uint8_t *)a.out + row * a.cols + c);
         };
-        float f[C > 0 ? C : 1][8];
+        // (silu(gate) up is kept; plain values are unpacked again, in half the registers)
+        float f[SWIGLU && C > 0 ? C : 1][8];
+        u32x4 v[C > 0 ? C : 1][SWIGLU ? 2 : 1];
         if constexpr (C > 0) {
-            u32x4 v[C][SWIGLU ? 2 : 1];
 #pragma unroll
             for (int i = 0; i < C; ++i) load(i, v[i]);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                values(v[i], f[i]);
-                largest(f[i]);
+                values(v[i], f[SWIGLU ? i : 0]);
+                largest(f[SWIGLU ? i : 0]);
             }
         } else {
             for (int i = 0; i < chunks; ++i) {
-                u32x4 v[SWIGLU ? 2 : 1];
-                load(i, v);
-                values(v, f[0]);
+                load(i, v[0]);
+                values(v[0], f[0]);
                 largest(f[0]);
             }
         }
@@ -450,12 +563,14 @@ __global__ __launch_bounds__(kThreads) void k_row_int8(RowsArgs a) {
         const float am = fmaxf(m, 1e-30f), inv = 127.0f / am;
         if constexpr (C > 0) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) write(i, f[i], inv, bad);
+            for (int i = 0; i < C; ++i) {
+                if (!SWIGLU) values(v[i], f[0]);
+                write(i, f[SWIGLU ? i : 0], inv, bad);
+            }
         } else {
             for (int i = 0; i < chunks; ++i) {
-                u32x4 v[SWIGLU ? 2 : 1];
-                load(i, v);
-                values(v, f[0]);
+                load(i, v[0]);
+                values(v[0], f[0]);
                 write(i, f[0], inv, bad);
             }
         }
@@ -698,14 +813,14 @@ int ep_quantize_mxint8(const ep_groups *groups, const uint16_t *x, int64_t num_r
     if (ep::overlap(q, n, x, n * 2) || ep::overlap(scales, n / 32, x, n * 2) || ep::overlap(q, n, scales, n / 32))
         return EP_ERR_ARG;
     if (int r = ep::device_cus(&cus)) return r;
+    a.a = x;
+    a.out = q;
+    a.scales = scales;
     if (!groups) {  // dense rows are one long one
         a.cols = num_rows * cols;
         a.num_rows = rows = 1;
     }
-    a.a = x;
-    a.out = q;
-    a.scales = scales;
-    return ep::hip_status(launch_rows<kQuantizeMx8>(a, rows, cus, (hipStream_t)stream), "ep_quantize_mxint8");
+    return ep::hip_status(launch_segments<kQuantizeMx8, 8>(a, rows, cus, (hipStream_t)stream), "ep_quantize_mxint8");
 }
 
 int ep_dequantize_mxint8(const ep_groups *groups, const int8_t *q, const uint8_t *scales, int64_t num_rows, int cols,
@@ -728,7 +843,7 @@ int ep_dequantize_mxint8(const ep_groups *groups, const int8_t *q, const uint8_t
     a.q = (const uint8_t *)q;
     a.qs = scales;
     a.out = x;
-    return ep::hip_status(launch_rows<kDequantizeMx8>(a, rows, cus, (hipStream_t)stream), "ep_dequantize_mxint8");
+    return ep::hip_status(launch_segments<kDequantizeMx8, 4>(a, rows, cus, (hipStream_t)stream), "ep_dequantize_mxint8");
 }
 
 int ep_swiglu_checkpoint(const ep_groups *groups, const uint16_t *gate_up, int64_t num_rows, int I, uint16_t *out,
@@ -751,7 +866,7 @@ int ep_swiglu_checkpoint(const ep_groups *groups, const uint16_t *gate_up, int64
     a.out = out;
     a.keep = (uint8_t *)q;
     a.scales = scales;
-    return ep::hip_status(launch_rows<kSwigluKeep>(a, rows, cus, (hipStream_t)stream), "ep_swiglu_checkpoint");
+    return ep::hip_status(launch_segments<kSwigluKeep, 4>(a, rows, cus, (hipStream_t)stream), "ep_swiglu_checkpoint");
 }
 
 int ep_swiglu_checkpoint_backward(const ep_groups *groups, const uint16_t *grad_out, const int8_t *q,
@@ -778,7 +893,7 @@ int ep_swiglu_checkpoint_backward(const ep_groups *groups, const uint16_t *grad_
     a.d = grad_out;
     a.out = grad_gate_up;
     a.again = out;
-    return ep::hip_status(launch_rows<kSwigluKeptGrad>(a, rows, cus, (hipStream_t)stream),
+    return ep::hip_status(launch_segments<kSwigluKeptGrad, 2>(a, rows, cus, (hipStream_t)stream),
                           "ep_swiglu_checkpoint_backward");
 }
 
