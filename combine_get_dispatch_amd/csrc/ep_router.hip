@@ -10,6 +10,12 @@
 // lanes finds value and index. Every lane sorts its own numbers once; each of
 // the k choices is then the maximum of the lanes' first ones, and the lane that
 // had it moves up.
+//
+// What bounds it, on MI355X: few tokens a launch and the chain of k maxima (128
+// tokens x 256 experts, k = 8: 3.7 us, an empty kernel 2.3); many tokens the vector
+// instructions, which for 64-bit numbers of every expert took twice the time of
+// the candidates' form (k_route_many). Memory would allow 3.5 us for the 18 MB of
+// 16384 tokens x 256 experts in fp32.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -47,7 +53,6 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t from_lane(uint32_t v) {
     return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
-
 
 // `op` of a value with that of the lane 1, 2, 4, 8, 16, 32 away (STEP 0 to 5;
 // a mirror image from step 2 on, where the lanes nearer already hold the same)
@@ -461,7 +466,8 @@ __device__ __forceinline__ double sort16(double v, int sub) {
 // bounds the k-th largest of all from below, and what may reach it, some 8 to 12
 // experts (more where many logits are equal), goes to a lane each, 16 at a time,
 // to be ordered by the exact numbers. Groups are ordered by 32 bits where those
-// decide, else exactly.
+// decide, else exactly. 16384 tokens x 256 experts in fp32, k = 8: sigmoid in groups
+// with a bias 11.9 us (22.4 by k_route), softmax 8.9 (12.7).
 __host__ __device__ constexpr int place(int e) { return e + e / 16 * 4; }
 
 template <int P, bool BF16>
@@ -666,8 +672,9 @@ constexpr int kGradThreads = 256;
 // their places, and then written as a row (softmax that is not renormalized:
 // with every expert's share added). Lanes take V neighbours in turn, at most 16
 // in all. What bounds it is writing the row, and a launch's latency: 16384
-// tokens x 256 experts in fp32 6.6 us one by one, 6.3 in fours (softmax not renormalized
-// 13.3 and 7.9, its logits read once).
+// tokens x 256 experts in fp32 6.6 us one by one, 6.3 in fours (2.8 TB/s; softmax
+// not renormalized 13.3 and 7.9, its logits read once: 4.4 TB/s). 173 tokens x 48
+// experts 3.5 us: a launch, and two loads that depend on each other.
 template <int L, bool BF16, int V>
 __global__ __launch_bounds__(kGradThreads) void k_route_grad(GradArgs a) {
     constexpr int kRow = L * 16, kTurns = 16 / V;

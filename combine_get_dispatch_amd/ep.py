@@ -1038,12 +1038,13 @@ def _quantized(x, groups, out, call, dtype, scale_shape, scale_dtype):
     p = _tensor(x, "x", _torch.bfloat16, x.shape, dev)
     shape = tuple(x.shape)
     scale_shape = scale_shape(shape) if shape else ()
-    if out is None:
-        out = _torch.empty(shape, dtype=dtype, device=x.device), _torch.empty(scale_shape, dtype=scale_dtype,
-                                                                              device=x.device)
-    q, scales = out
-    call(None if groups is None else groups._c(dev), p, n, cols, _tensor(q, "q", dtype, shape, dev),
-         _tensor(scales, "scales", scale_dtype, scale_shape, dev), _raw_stream(dev))
+    if out is None:  # (what a call allocates itself needs no checks: 0.35 us each)
+        q, scales = x.new_empty(shape, dtype=dtype), x.new_empty(scale_shape, dtype=scale_dtype)
+        to, scales_to = q.data_ptr(), scales.data_ptr()
+    else:
+        q, scales = out
+        to, scales_to = _tensor(q, "q", dtype, shape, dev), _tensor(scales, "scales", scale_dtype, scale_shape, dev)
+    call(None if groups is None else groups._c(dev), p, n, cols, to, scales_to, _raw_stream(dev))
     return q, scales
 
 
@@ -1074,9 +1075,11 @@ def dequantize_mxint8(q, scales, groups: Optional[Groups] = None, out=None):
     p = _tensor(q, "q", _torch.int8, shape, dev)
     s = _tensor(scales, "scales", _torch.uint8, shape[:-1] + (cols // 32,), dev)
     if out is None:
-        out = _torch.empty(shape, dtype=_torch.bfloat16, device=q.device)
-    ep_dequantize_mxint8(None if groups is None else groups._c(dev), p, s, n, cols,
-                         _tensor(out, "out", _torch.bfloat16, shape, dev), _raw_stream(dev))
+        out = q.new_empty(shape, dtype=_torch.bfloat16)
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", _torch.bfloat16, shape, dev)
+    ep_dequantize_mxint8(None if groups is None else groups._c(dev), p, s, n, cols, to, _raw_stream(dev))
     return out
 
 
@@ -1169,10 +1172,13 @@ def route(logits, router: Router, bias=None, out=None):
     b = None if bias is None else _tensor(bias, "bias", _torch.float32, (router.num_experts,), dev)
     shape = (T, router.num_topk)
     if out is None:
-        out = logits.new_empty(shape, dtype=_torch.int32), logits.new_empty(shape, dtype=_torch.float32)
-    idx, w = out
-    ep_route(r, p, logits.dtype is _torch.float32, b, T, _tensor(idx, "topk_idx", _torch.int32, shape, dev),
-             _tensor(w, "topk_weights", _torch.float32, shape, dev), _raw_stream(dev))
+        idx, w = logits.new_empty(shape, dtype=_torch.int32), logits.new_empty(shape, dtype=_torch.float32)
+        idx_to, w_to = idx.data_ptr(), w.data_ptr()
+    else:
+        idx, w = out
+        idx_to = _tensor(idx, "topk_idx", _torch.int32, shape, dev)
+        w_to = _tensor(w, "topk_weights", _torch.float32, shape, dev)
+    ep_route(r, p, logits.dtype is _torch.float32, b, T, idx_to, w_to, _raw_stream(dev))
     return idx, w
 
 
@@ -1189,8 +1195,10 @@ def route_backward(grad_weights, logits, topk_idx, router: Router, out=None):
     idx = _tensor(topk_idx, "topk_idx", _torch.int32, shape, dev)
     if out is None:
         out = _torch.empty_like(logits)
-    ep_route_backward(r, p, logits.dtype is _torch.float32, idx, d, T,
-                      _tensor(out, "out", logits.dtype, logits.shape, dev), _raw_stream(dev))
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", logits.dtype, logits.shape, dev)
+    ep_route_backward(r, p, logits.dtype is _torch.float32, idx, d, T, to, _raw_stream(dev))
     return out
 
 

@@ -129,6 +129,42 @@ def test_masks_and_ends(score, renorm, groups, with_bias):
         assert not torch.isin(idx, torch.tensor([9, 10], dtype=torch.int32, device="cuda")).any()
 
 
+@pytest.mark.parametrize("T", [2050, 4100])
+@pytest.mark.parametrize("score,groups,with_bias", [("softmax", 1, False), ("softmax", 8, False), ("sigmoid", 1, True),
+                                                    ("sigmoid", 8, True), ("sigmoid", 8, False), ("softmax", 8, True)])
+def test_masks_and_ends_of_many_tokens(T, score, groups, with_bias):
+    """Masked, infinite, equal and NaN logits among the tokens of a batch that fills the chip: as in a small one."""
+    E, k = 64, 6
+    r = ep.Router(E, k, score=score, renormalize=groups == 1, num_groups=groups, topk_groups=max(1, groups // 2))
+    rng = np.random.default_rng([groups, int(with_bias), 7])
+    logits = drawn(rng, 16, E, torch.float32)
+    logits[0] = -INF
+    logits[1, 3:] = -INF
+    logits[2, ::2] = -INF
+    logits[3, 4:] = LOWEST
+    logits[4] = LOWEST
+    logits[5, [5, 40]] = INF
+    logits[6, 7] = float("nan")
+    logits[7] = float("nan")
+    logits[8, 1:] = -INF
+    logits[9] = 50.0 + torch.from_numpy(rng.standard_normal(E).astype(np.float32))  # sigmoids that are 1 in 32 bits
+    logits[10] = INF
+    logits[11, :8], logits[11, 8:] = 0.25, -INF
+    logits[12] = logits[12].round()
+    logits[13] = -200.0 + torch.from_numpy(rng.standard_normal(E).astype(np.float32))
+    b = None
+    if with_bias:
+        b = torch.from_numpy(rng.standard_normal(E, dtype=np.float32) * np.float32(0.1))
+        b[9], b[10], b[33], b[34], b[35] = -INF, float("nan"), 50.0, -50.0, 1e30
+    few, fw = check(logits, r, b)
+    at = torch.arange(T) % 16
+    idx, w = ep.route(logits[at].cuda(), r, bias=None if b is None else b.cuda())
+    assert torch.equal(idx, few[at.cuda()])
+    fw = torch.from_numpy(fw)[at].cuda()
+    assert torch.equal(w.isnan(), fw.isnan())
+    assert bool(((w - fw).abs().nan_to_num(0.0) <= 64 * 2.0 ** -24 * fw.nan_to_num(0.0) + 2.0 ** -120).all())
+
+
 @pytest.mark.parametrize("value", [-1e4, -200.0, 200.0, 1e4, LOWEST])
 def test_renormalized_weights_of_far_logits(value):
     """Scores that underflow (or are all 1) still give weights that sum to the scale."""
