@@ -369,14 +369,18 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
 // Its codes are in registers a step ahead: in a step's first half they are
 // widened and written to the next step's buffer, a code between two matrix
 // instructions (put), and a chunk that is done with is loaded again for the step
-// after (fetch). The vector instructions that this takes, 200 a step and wave,
-// are what it costs beside the bf16 form (1.7 against 1.5 ms): at their full rate
-// the matrix instructions leave a wave's others no time of their own. So a copy
-// of the codes to LDS first, all waits counted by hand, was no faster (1.83 ms),
-// nor were the same instructions spread over both halves (1.85). (The compiler
-// waits for the loads by itself. It counts no copies to LDS, and so waits for no
-// less than it has to: for a chunk's loads it asks that no more be in flight
-// than there are later loads.)
+// after (fetch). The vector instructions that this takes, some 3 a code, are what
+// it costs beside the bf16 form (32768 rows, 8 experts of 4096 x 7168: 1.60 against
+// 1.51 ms). A wave's matrix instructions at their full rate leave its others no
+// time of their own, another wave's do: eight waves of 128 x 64 results, two a
+// SIMD, in place of the four of 128 x 128 that suit bf16 (1.72 ms). No faster:
+// widening spread over both halves (1.64 ms: its loads come half a step ahead),
+// half of the waves copying and the others widening (1.75), the codes copied to
+// LDS first, all waits counted by hand (four waves: 1.80), 512 x 128 tiles (1.86),
+// bank conflicts of the writes taken out (1.60). (The compiler waits for the loads
+// by itself. It counts no copies to LDS, and so waits for no less than it has to:
+// for a chunk's loads it asks that no more be in flight than there are later
+// loads.)
 template <class P>
 __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
     constexpr int ACT = P::ACT, NT = P::NT, C = P::kPer, W = 16 * P::kChunks;
@@ -1349,7 +1353,7 @@ static int wgrad(const ep_groups *groups, const uint16_t *grad_out, const void *
     hipError_t e;
     if (kept)
         e = a.g.region_rows > 0 ? launch_wgrad<128, 128, 2, 2, true, true>(a, cus, s)
-            : wide              ? launch_wgrad<256, 256, 2, 2, false, true>(a, cus, s)
+            : wide              ? launch_wgrad<256, 256, 2, 4, false, true>(a, cus, s)
                                 : launch_wgrad<128, 128, 2, 2, false, true>(a, cus, s);
     else
         e = a.g.region_rows > 0 ? launch_wgrad<128, 128, 2, 2, true, false>(a, cus, s)

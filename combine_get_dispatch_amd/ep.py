@@ -1093,14 +1093,16 @@ def swiglu_checkpoint(gate_up, groups: Optional[Groups] = None, out=None, kept=N
     I //= 2
     x = _tensor(gate_up, "gate_up", _torch.bfloat16, (n, 2 * I), dev)
     if out is None:
-        out = _torch.empty((n, I), dtype=_torch.bfloat16, device=gate_up.device)
+        out = gate_up.new_empty((n, I))
+    o = _tensor(out, "out", _torch.bfloat16, (n, I), dev)
     if kept is None:
-        kept = (_torch.empty((n, 2 * I), dtype=_torch.int8, device=gate_up.device),
-                _torch.empty((n, I // 16), dtype=_torch.uint8, device=gate_up.device))
-    q, scales = kept
-    ep_swiglu_checkpoint(None if groups is None else groups._c(dev), x, n, I,
-                         _tensor(out, "out", _torch.bfloat16, (n, I), dev), _tensor(q, "q", _torch.int8, (n, 2 * I), dev),
-                         _tensor(scales, "scales", _torch.uint8, (n, I // 16), dev), _raw_stream(dev))
+        q, scales = gate_up.new_empty((n, 2 * I), dtype=_torch.int8), gate_up.new_empty((n, I // 16), dtype=_torch.uint8)
+        to, scales_to = q.data_ptr(), scales.data_ptr()
+    else:
+        q, scales = kept
+        to = _tensor(q, "q", _torch.int8, (n, 2 * I), dev)
+        scales_to = _tensor(scales, "scales", _torch.uint8, (n, I // 16), dev)
+    ep_swiglu_checkpoint(None if groups is None else groups._c(dev), x, n, I, o, to, scales_to, _raw_stream(dev))
     return out, q, scales
 
 
