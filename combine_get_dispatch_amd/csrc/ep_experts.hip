@@ -14,7 +14,8 @@
 //
 // Two shapes. 256 rows x 256 channels, one workgroup per CU: four waves of 128
 // x 128 results, the fewest LDS bytes per product that the registers allow
-// (FP8, whose sums pass through vector registers to be scaled: eight waves of
+// (FP8 and 8-bit integers, whose sums pass through vector registers to be scaled,
+// and weight gradients of rows kept in 8 bits, which are widened: eight waves of
 // 128 x 64). 128 x 128, two workgroups per CU, where an expert has few rows
 // and the weights' bytes are the time. On MI355X: gradients of 32768 rows, 8
 // experts of 4096 x 7168: 1.27 PFLOP/s (a library product of that size 1.52);
@@ -237,12 +238,8 @@ __device__ __forceinline__ void mfma_bf16(i32x4 a, i32x4 b, f32x4 &c) {
 }
 
 // the same of 8-bit integers: c holds 32-bit integers
-template <bool ACC>
 __device__ __forceinline__ void mfma_int8(i32x4 a, i32x4 b, f32x4 &c) {
-    if constexpr (ACC)
-        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : EP_ACC(c) : "v"(a), "v"(b));
-    else
-        c = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(i32x4, c), 0, 0, 0));
+    c = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(i32x4, c), 0, 0, 0));
 }
 
 // as: the scale byte of the lane's 32 values of a, in the word's low byte
@@ -384,7 +381,7 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
 template <class P>
 __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int whole, f32x4 (&acc)[P::ACT][P::NT]) {
     constexpr int ACT = P::ACT, NT = P::NT, C = P::kPer, W = 16 * P::kChunks;
-    static_assert(P::kStages == 2, "two buffers");
+    static_assert(P::kStages == 2 && !P::kAcc, "two buffers, accumulators that the compiler assigns");
     const uint32_t other = ring + P::kStage;
     if constexpr (P::kTable) {
         for (int i = 0; i < 3; ++i) p.look_up(i);
@@ -437,7 +434,6 @@ __device__ __forceinline__ void reduce_kept(P &p, uint32_t ring, int steps, int 
             p.mfma(h1, m / NT, m % NT, acc[m / NT][m % NT]);
             if (m % 2) pin();
         }, std::make_integer_sequence<int, M>());
-        if (P::kAcc && COPIES == kLast) settle();
         const uint32_t t = st;
         st = nx;
         nx = t;
@@ -794,7 +790,7 @@ struct Product {
             if constexpr (FORM == kMx4)
                 mfma_mx4<kAcc>(h.w[j], h.x[i], c, h.ws[j], h.xs[i]);
             else if constexpr (FORM == kInt8)
-                mfma_int8<kAcc>(h.w[j], h.x[i], c);
+                mfma_int8(h.w[j], h.x[i], c);
             else
                 mfma_bf16<kAcc>(h.w[j], h.x[i], c);
         }
@@ -819,9 +815,9 @@ struct Product {
             reduce(t, ring, a.steps, t.row_bytes / kStepBytes, acc);
         }
         // 8-bit integers: a lane's four channels of a column tile have four scales (past the last channel: any), its row of a row
-        // tile one. All are loaded before the first store, behind which the compiler would wait for each (32768 ragged rows, 64
-        // experts of 4096 x 7168 and back: 1090 and 658 us in place of 1051 and 610; by way of LDS, loaded before the reduction,
-        // 1079 and 652).
+        // tile one. All are loaded before the first store, behind which the compiler would wait for each (four waves, 32768 ragged
+        // rows, 64 experts of 4096 x 7168 and back: 1090 and 658 us in place of 1051 and 610; by way of LDS, loaded before the
+        // reduction, 1079 and 652).
         f32x4 ws[FORM == kInt8 ? NTILES : 1];
         float xs[FORM == kInt8 ? ACT : 1];
         if constexpr (FORM == kInt8) {
@@ -1210,13 +1206,16 @@ hipError_t launch_product(const ProductArgs &a, int grid, hipStream_t s) {
 // 256-channel tiles of up to 256 rows where the experts have rows for them and
 // there are enough for the chip, else 128-channel tiles of up to 128 rows, two
 // workgroups to a CU: where the weights' bytes are the time, one streams while
-// the other starts or ends its tile.
+// the other starts or ends its tile. 8-bit integers: eight waves, of which two a
+// SIMD scale and write results side by side (32768 ragged rows, 64 experts of 4096
+// x 7168 and back: 1018 and 553 us; four waves 1058 and 621; on 8 experts, even,
+// 764 and 464 against 803 and 528; a library product of the first size 822).
 template <int FORM, bool WTR>
 hipError_t launch_product_form(const ProductArgs &a, int64_t rows, int cus, hipStream_t s) {
     const int64_t experts = rows < a.g.E ? rows : a.g.E;
     const int64_t big = (rows / 256 > experts ? rows / 256 : experts) * ((a.N + 255) / 256);
     if (rows > 64 * (int64_t)a.g.E && big >= cus)
-        return launch_product<FORM, WTR, 256, 2, FORM == kFp8 ? 4 : 2, 8>(a, cus, s);
+        return launch_product<FORM, WTR, 256, 2, FORM == kFp8 || FORM == kInt8 ? 4 : 2, 8>(a, cus, s);
     const int64_t most = (rows / 32 + experts) * ((a.N + 127) / 128);
     return launch_product<FORM, WTR, 128, 2, 2, 4>(a, (int)(most < 2 * cus ? most : 2 * cus), s);
 }
