@@ -35,6 +35,23 @@ bf16 and MXFP4 likewise, and the bf16 gradients)::
     a, a_scales = ep.swiglu(h, g, kind="fp8")
     expert_out = ep.expert_gemm(a, w2, g, row_scales=a_scales, weight_scales=s2)
 
+The router before the dispatch, the same layer in 8-bit integers, and training
+that keeps its activations in 8 bits::
+
+    r = ep.Router(num_experts, num_topk, score="sigmoid", num_groups=8, topk_groups=4, scale=2.5)
+    topk_idx, topk_w = ep.route(logits, r, bias=bias)      # ready for the dispatch calls
+    grad_logits = ep.route_backward(grad_w, logits, topk_idx, r)
+
+    q, s = ep.quantize_int8(rows, g)                       # weights once: ep.quantize_int8(w13)
+    h = ep.expert_gemm(q, w13, g, row_scales=s, weight_scales=s13)
+    a, a_scales = ep.swiglu(h, g, kind="int8")
+    expert_out = ep.expert_gemm(a, w2, g, row_scales=a_scales, weight_scales=s2)
+
+    x_kept, x_scales = ep.quantize_mxint8(rows, g)         # rows need not be held
+    a, h_kept, h_scales = ep.swiglu_checkpoint(h, g)       # nor h, nor a
+    grad_h, a = ep.swiglu_checkpoint_backward(grad_a, h_kept, h_scales, g)
+    grad_w13 = ep.expert_gemm_wgrad(grad_h, x_kept, g, row_scales=x_scales)
+
 The rank-deduplicated exchange (``dispatch_dedup_with_layout``: one row per
 (token, destination rank) with the row's local expert indices and weights)
 and the low-latency form (``dispatch_low_latency``: fixed per-(expert,
