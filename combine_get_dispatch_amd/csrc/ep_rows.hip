@@ -495,7 +495,9 @@ hipError_t launch_segments(const RowsArgs &a, int64_t rows, int cus, hipStream_t
 // silu(gate) up in place of the values. On MI355X: 32768 rows x 7168 113 us (705
 // MB, 6.2 TB/s), SwiGLU of 32768 rows x 2048 60 us (336 MB, 5.6 TB/s; its vector
 // instructions are issued in 86% of the SIMDs' cycles), 1024 rows in the
-// low-latency layout 10.1 and 8.6 us, a launch and one row's way.
+// low-latency layout 10.1 and 8.6 us, a launch and one row's way. (16 chunks a
+// lane: registers for three waves a SIMD; left to the compiler 133 us in place of
+// 113, for four 206.)
 template <int C, bool SWIGLU>
 __global__ __launch_bounds__(kThreads, C >= 16 ? 3 : 1) void k_row_int8(RowsArgs a) {
     __shared__ int ends[ep::kGroupsMaxExperts];
@@ -583,6 +585,9 @@ __global__ __launch_bounds__(kThreads, C >= 16 ? 3 : 1) void k_row_int8(RowsArgs
     }
 }
 
+// The fewest chunks in registers that hold a row; beyond 16 (SwiGLU, whose values
+// are kept in 32 bits: 8) it is read twice (32768 rows x 7168: 204 us in place of
+// 113, 1024 rows 23 in place of 10).
 template <bool SWIGLU>
 hipError_t launch_row_int8(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
     const int64_t blocks = (rows + kThreads / 64 - 1) / (kThreads / 64), most = (int64_t)cus * kBlocksPerCu;
