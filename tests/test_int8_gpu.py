@@ -193,3 +193,62 @@ def test_layer():
                 gu = v1[e] @ x[t].double()
                 ref[t] += float(w[t, j]) * (v2[e] @ (gu[:I] * torch.sigmoid(gu[:I]) * gu[I:]))
     assert float((outs[0].double() - ref).norm() / ref.norm()) < 0.03
+
+
+def test_rows_past_32_bits():
+    """Rows whose places in the arrays pass 32 bits: as the same rows near the start."""
+    K, N, cap = 7168, 4096, 700000
+    counts, off = [40, 70], [cap - 200000, cap - 90]
+    g = ep.Groups(*(torch.tensor(v, dtype=torch.int32).cuda() for v in (counts, off)), num_experts=2, num_ranks=1, cap_rows=cap)
+    near = ep.Groups(g.counts, torch.tensor([0, 40], dtype=torch.int32).cuda(), num_experts=2, num_ranks=1, cap_rows=110)
+    rng = np.random.default_rng(10)
+    at = torch.cat([torch.arange(o, o + c) for o, c in zip(off, counts)]).cuda()
+    few = xh.bf16(rng, (110, K)).cuda()
+    x, out, a = (torch.empty((cap, c), dtype=torch.bfloat16, device="cuda") for c in (K, N, N // 2))
+    q, aq = (torch.empty((cap, c), dtype=torch.int8, device="cuda") for c in (K, N // 2))
+    s, s2 = (torch.empty(cap, device="cuda") for _ in range(2))
+    w, ws = ep.quantize_int8(xh.bf16(rng, (2, N, K), 0.05).cuda())
+    x[at] = few
+    ep.quantize_int8(x, g, out=(q, s))
+    ep.expert_gemm(q, w, g, row_scales=s, weight_scales=ws, out=out)
+    ep.swiglu(out, g, kind="int8", out=(aq, s2))
+    nq, ns = ep.quantize_int8(few)
+    h = ep.expert_gemm(nq, w, near, row_scales=ns, weight_scales=ws)
+    for far, want in zip((q, s, out, aq, s2), (nq, ns, h) + ep.swiglu(h, kind="int8")):
+        assert torch.equal(far[at], want)
+
+
+def test_calls_at_once():
+    """The layer and the router on four streams at once: each the result it has alone."""
+    rng = np.random.default_rng(11)
+    E, K, I = 8, 1024, 512
+    w1, w2 = (ep.quantize_int8(xh.bf16(rng, s, 0.05).cuda()) for s in ((E, 2 * I, K), (E, K, I)))
+    r = ep.Router(64, 6, score="sigmoid", num_groups=8, topk_groups=4)
+
+    def work(x, g, logits):
+        idx, wt = ep.route(logits, r)
+        q, s = ep.quantize_int8(x, g)
+        a, t = ep.swiglu(ep.expert_gemm(q, w1[0], g, row_scales=s, weight_scales=w1[1]), g, kind="int8")
+        y = ep.expert_gemm(a, w2[0], g, row_scales=t, weight_scales=w2[1])
+        k, ks = ep.quantize_mxint8(x, g)
+        return idx, wt, ep.route_backward(wt, logits, idx, r), y, ep.expert_gemm_wgrad(y, k, g, row_scales=ks)
+
+    cases = []
+    for i in range(4):
+        counts = [int(n) for n in rng.integers(0, 200, E)]
+        off = [sum(counts[:e]) for e in range(E)]
+        g = ep.Groups(*(torch.tensor(v, dtype=torch.int32).cuda() for v in (counts, off)), num_experts=E, num_ranks=1,
+                      cap_rows=sum(counts))
+        cases.append((xh.bf16(rng, (sum(counts), K)).cuda(), g,
+                      torch.from_numpy(rng.standard_normal((300 + 3000 * i, 64), dtype=np.float32)).cuda()))
+    alone = [work(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], []
+    for s, c in zip(streams, cases):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(work(*c))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
