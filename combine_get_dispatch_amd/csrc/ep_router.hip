@@ -558,19 +558,21 @@ __global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
         if (a.lg > 1) merge(std::integral_constant<int, 0>());
         if (a.lg > 2) merge(std::integral_constant<int, 1>());
         if (a.lg > 4) merge(std::integral_constant<int, 2>());
-        // the group's value, and how far apart two have to be for 32 bits to tell: without a bias a largest logit is exact (but
-        // a tie is left to the exact form), and scores that underflow are never told apart
-        float value = g1, far = 0.0f;
+        // The group's value and what 32 bits may be off of it. With a bias, each score: 2^-22; both numbers, their sum and the
+        // bounds below: a rounding each, 2^-24 of what was added, by its size, since biases of opposite signs leave a small sum.
+        // Without a bias a largest logit is exact, and scores that underflow are never told apart.
+        float value = g1, off = 0.0f;
         if (a.exact) {
-            value = fminf(a.top == 2 && g2 > -INFINITY ? g1 + g2 : g1, kMost);
-            far = 0x1p-20f + 0x1p-21f * fabsf(value);
+            const float more = a.top == 2 && g2 > -INFINITY ? g2 : 0.0f;
+            value = fminf(g1 + more, kMost);
+            off = 0x1p-21f + 0x1.9p-23f * fabsf(g1) + 0x1.9p-23f * fabsf(more);
         } else if (a.top == 2) {
             auto score = [&](float x) __attribute__((always_inline)) {
                 if (a.sigmoid) return exp32(fminf(x, 0.0f)) / sigmoid_den(x);
                 return exp32(x == top ? 0.0f : x - top);
             };
             value = g1 > -INFINITY ? score(g1) + (g2 > -INFINITY ? score(g2) : 0.0f) : -INFINITY;
-            far = 0x1p-19f * value + 0x1p-100f;
+            off = 0x1p-20f * value + 0x1p-100f;
         }
         const int mark = ordered(value);
         int left = mark, last = 0;
@@ -579,11 +581,13 @@ __global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
             left = left == last ? ordered(-INFINITY) : left;
         }
         bool closed = mark < last;
-        // the first group that does not stay may be too near the last that does; equal ones were counted once
-        const float gap = of_ordered(last) - of_ordered(max16(left));
-        const bool in = !closed && value > -INFINITY;
+        // sure if those that stay are not too many (equal ones were counted once) and the least that each can be is more than the
+        // most that any other can be
+        const bool open = value > -INFINITY, in = open && !closed;
         const int stay = __popcll(__ballot(in && (sub & (a.lg - 1)) == 0) >> (lane & 48) & 0xFFFF);
-        const bool unsure = in && (stay > a.kept || (mark == last && gap <= far));
+        const float least_in = -of_ordered(max16(ordered(in ? off - value : -INFINITY)));
+        const float most_out = of_ordered(max16(ordered(open && closed ? value + off : -INFINITY)));
+        const bool unsure = in && (stay > a.kept || !(least_in > most_out));
         if (__builtin_expect(__ballot(unsure) != 0, 0)) {  // some group of the wave's tokens: all its groups exactly
             double d1 = minus_inf(), d2 = minus_inf();
 #pragma unroll 1
