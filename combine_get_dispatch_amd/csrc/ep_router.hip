@@ -560,7 +560,9 @@ __global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
         if (a.lg > 4) merge(std::integral_constant<int, 2>());
         // The group's value and what 32 bits may be off of it. With a bias, each score: 2^-22; both numbers, their sum and the
         // bounds below: a rounding each, 2^-24 of what was added, by its size, since biases of opposite signs leave a small sum.
-        // Without a bias a largest logit is exact, and scores that underflow are never told apart.
+        // Without a bias a largest logit is exact; the sum of two scores is off by 9 roundings at most (exponential 3, quotient
+        // and denominator 4, sum, bounds), softmax's by its logits' differences' too, 2^-24 of a difference, by which the
+        // exponential grows. Scores that underflow are never told apart.
         float value = g1, off = 0.0f;
         if (a.exact) {
             const float more = a.top == 2 && g2 > -INFINITY ? g2 : 0.0f;
@@ -569,10 +571,12 @@ __global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
         } else if (a.top == 2) {
             auto score = [&](float x) __attribute__((always_inline)) {
                 if (a.sigmoid) return exp32(fminf(x, 0.0f)) / sigmoid_den(x);
-                return exp32(x == top ? 0.0f : x - top);
+                const float far = x == top ? 0.0f : x - top, y = exp32(far);
+                off = fmaf(y, fminf(-far, 128.0f), off);
+                return y;
             };
             value = g1 > -INFINITY ? score(g1) + (g2 > -INFINITY ? score(g2) : 0.0f) : -INFINITY;
-            off = 0x1p-20f * value + 0x1p-100f;
+            off = 0x1p-24f * off + 0x1.4p-21f * value + 0x1p-100f;
         }
         const int mark = ordered(value);
         int left = mark, last = 0;

@@ -50,3 +50,23 @@ def test_biases_of_opposite_signs(B, both, size):
     assert len(x) == T
     r = ep.Router(4 * size, 4, score="sigmoid", num_groups=4, topk_groups=2)
     same_choice(x.reshape(T, -1), r, bias.reshape(-1))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("below", [0, 10, 20, 30, 45, 60, 80])
+def test_logits_far_below_the_largest(score, below):
+    """No bias: of four groups the first has the largest logit and the others' lie `below` under it, where the difference of two
+    logits is rounded by more than a score's other roundings; two of them nearly tie."""
+    rng = np.random.default_rng([below, int(score == "softmax")])
+    of = np.exp if score == "softmax" else sigmoid
+    x = (rng.standard_normal((4 * T, 4, 2)) - below / 2).astype(np.float32)
+    x[:, 0, 0] = below / 2 + rng.random(4 * T)
+    x[:, 3] -= 5
+    s = of(x.astype(np.float64))
+    first = s[:, 1].sum(1)
+    last = first * (1 + rng.choice([-1, 1], 4 * T) * np.exp2(rng.uniform(-24, -16, 4 * T))) - s[:, 2, 0]
+    good = (last > 1e-3 * first) & (last < 0.99 if score == "sigmoid" else True)
+    x, last = x[good][:T], last[good][:T]
+    x[:, 2, 1] = np.log(last) if score == "softmax" else np.log(last) - np.log1p(-last)
+    assert len(x) == T
+    same_choice(x.reshape(T, 8), ep.Router(8, 4, score=score, num_groups=4, topk_groups=2))
