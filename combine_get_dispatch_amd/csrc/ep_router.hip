@@ -566,7 +566,7 @@ __global__ __launch_bounds__(256) void k_route_many(RouteArgs a) {
         float value = g1, off = 0.0f;
         if (a.exact) {
             const float more = a.top == 2 && g2 > -INFINITY ? g2 : 0.0f;
-            value = fminf(g1 + more, kMost);
+            value = g1 > -INFINITY ? fminf(fmaxf(g1 + more, -kMost), kMost) : -INFINITY;  // (beyond the range: all the same)
             off = 0x1p-21f + 0x1.9p-23f * fabsf(g1) + 0x1.9p-23f * fabsf(more);
         } else if (a.top == 2) {
             auto score = [&](float x) __attribute__((always_inline)) {

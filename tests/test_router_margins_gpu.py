@@ -70,3 +70,15 @@ def test_logits_far_below_the_largest(score, below):
     x[:, 2, 1] = np.log(last) if score == "softmax" else np.log(last) - np.log1p(-last)
     assert len(x) == T
     same_choice(x.reshape(T, 8), ep.Router(8, 4, score=score, num_groups=4, topk_groups=2))
+
+
+def test_biases_near_the_lowest_number():
+    """Groups' sums beyond the lowest 32-bit number: these groups are open, and in order among each other."""
+    low = float(np.finfo(np.float32).min)
+    bias = np.array([0.5, 0.25, low, low, -1e38, -3e38, -2.9e38, -2.95e38], np.float32)
+    logits = np.random.default_rng(1).standard_normal((T, 8)).astype(np.float32)
+    r = ep.Router(8, 4, score="sigmoid", num_groups=4, topk_groups=2)
+    want, _ = rh.route(logits[:1], r, bias)
+    assert sorted(want[0]) == [0, 1, 4, 5]
+    same_choice(logits, r, bias)
+    same_choice(logits, ep.Router(8, 3, score="sigmoid", num_groups=4, topk_groups=2), np.full(8, low, np.float32))
