@@ -1345,7 +1345,9 @@ static int wgrad(const ep_groups *groups, const uint16_t *grad_out, const void *
     // 256 x 256 tiles where there are enough for the chip and rows enough to sum, else 128 x 128 (48 experts of 7 rows,
     // 126 MB of fp32 results: 27.5 us against 58; 8 experts of 4096 rows, 4096 x 7168: 1.5 ms against 2.4). The low-latency
     // layout takes the small tile: its rows are looked up for each copy, which keeps the loop from being unrolled and puts
-    // the accumulators into scratch memory (2048 rows on 64 experts of 4096 x 2048: 3.1 ms against 0.6 for packed rows)
+    // the accumulators into scratch memory (2048 rows on 64 experts of 4096 x 2048: 3.1 ms against 0.6 for packed rows). Rows
+    // kept in 8 bits are looked up once a step (that size to bf16 results: 0.42 ms, packed 0.36; 32768 rows, 8 experts of 4096
+    // x 7168, 4.1 and 1.6)
     const int64_t big = (int64_t)a.g.E * ((N + 255) / 256) * ((K + 255) / 256);
     const bool wide = big >= cus && ep::group_rows_expected(groups) >= 128 * (int64_t)a.g.E;
     const hipStream_t s = (hipStream_t)stream;

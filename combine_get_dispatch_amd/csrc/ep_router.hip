@@ -12,10 +12,15 @@
 // had it moves up.
 //
 // What bounds it, on MI355X: few tokens a launch and the chain of k maxima (128
-// tokens x 256 experts, k = 8: 3.7 us, an empty kernel 2.3); many tokens the vector
-// instructions, which for 64-bit numbers of every expert took twice the time of
-// the candidates' form (k_route_many). Memory would allow 3.5 us for the 18 MB of
-// 16384 tokens x 256 experts in fp32.
+// tokens x 256 experts, k = 8: 3.7 us, an empty kernel 2.3); many tokens chains of
+// lane exchanges and vector instructions (issued in 60% of the SIMDs' cycles, waves
+// waiting in 49% of theirs), which for 64-bit numbers of every expert took twice the
+// time of the candidates' form (k_route_many). Memory would allow 2.5 us for the 18
+// MB of 16384 tokens x 256 experts in fp32. What the candidates' form does not take
+// (more than 256 experts or 8 choices, softmax with a bias), 16384 tokens in fp32: 256
+// experts, softmax with a bias, k = 8, 21.4 us, sigmoid with one, k = 10, 26.4; 384
+// experts with a bias, k = 8, 34.4, in groups 37.8; 512 experts, k = 10, 26.7 (2.5,
+// 2.6, 3.7 and 5.0 by memory).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -466,8 +471,11 @@ __device__ __forceinline__ double sort16(double v, int sub) {
 // bounds the k-th largest of all from below, and what may reach it, some 8 to 12
 // experts (more where many logits are equal), goes to a lane each, 16 at a time,
 // to be ordered by the exact numbers. Groups are ordered by 32 bits where those
-// decide, else exactly. 16384 tokens x 256 experts in fp32, k = 8: sigmoid in groups
-// with a bias 11.9 us (22.4 by k_route), softmax 8.9 (12.7).
+// decide, else exactly. 16384 tokens x 256 experts in fp32, k = 8: softmax 8.9 us
+// (12.7 by k_route), in groups 9.8; sigmoid in groups with a bias 9.0 where 32 bits
+// decide every token's groups, 10.5 to 13.3 with one to three tokens where they do not
+// (one in some 15000 of normal logits; their waves end last), 22.4 by k_route. With
+// biases of 1000 and -1000 by turns, one token in 200 undecided, 18.1.
 __host__ __device__ constexpr int place(int e) { return e + e / 16 * 4; }
 
 template <int P, bool BF16>

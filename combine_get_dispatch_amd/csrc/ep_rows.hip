@@ -446,7 +446,12 @@ __device__ __forceinline__ void write_scales(const RowsArgs &a, int64_t row, int
 // input, 65536 rows x 2048, 200 us chunk by chunk and 179 by fours.) On MI355X,
 // memory bounds all four: that quantization 113 us (6.3 TB/s), of 16384 rows 55.5
 // and back 56.6 us (6.4 and 6.3), SwiGLU that keeps 179 us (6.0), its gradient with
-// the forward result 218 us (6.2; 232 with a fourth of the workgroups).
+// the forward result 218 us (6.2; 232 with a fourth of the workgroups). C is the same
+// for every width (dense rows are one long row): in groups, a segment past its row's
+// end computes chunks that are not stored. TB/s of 134e6 values in rows of 2048, 1408,
+// 768, 512 and 128 channels: quantization 5.6, 5.0, 3.6, 2.8, 1.0, back 6.2, 6.0, 4.5,
+// 3.5, 1.5, SwiGLU that keeps 6.2, 5.9, 5.4, 5.1, 1.8, its gradient 6.2, 6.1, 6.1, 5.9,
+// 2.3.
 template <int OP, int C>
 __global__ __launch_bounds__(kThreads) void k_segments(RowsArgs a) {
     __shared__ int ends[ep::kGroupsMaxExperts];
@@ -586,8 +591,9 @@ __global__ __launch_bounds__(kThreads, C >= 16 ? 3 : 1) void k_row_int8(RowsArgs
 }
 
 // The fewest chunks in registers that hold a row; beyond 16 (SwiGLU, whose values
-// are kept in 32 bits: 8) it is read twice (32768 rows x 7168: 204 us in place of
-// 113, 1024 rows 23 in place of 10).
+// are kept in 32 bits: 8) it is read twice (32768 rows x 7168 so: 204 us in place of
+// 113, 1024 rows 23 in place of 10; rows that need it: 16384 x 14336 203 us, 3.5 TB/s,
+// SwiGLU of 16384 x 8192 213 us, 3.2 TB/s, computed twice).
 template <bool SWIGLU>
 hipError_t launch_row_int8(const RowsArgs &a, int64_t rows, int cus, hipStream_t s) {
     const int64_t blocks = (rows + kThreads / 64 - 1) / (kThreads / 64), most = (int64_t)cus * kBlocksPerCu;

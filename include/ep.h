@@ -602,7 +602,8 @@ int ep_expert_gemm_wgrad_mxint8(const ep_groups *groups, const uint16_t *grad_ou
  * of their experts the num_topk with the largest c_e, in that order. Ties go to
  * the lower index, of groups and of experts. The order is that of the exact
  * scores: without a bias the logits are compared, with one 64-bit c_e, of which
- * the leading 43 bits count; groups' sums are 64-bit numbers.
+ * the leading 43 bits count; groups' values are 64-bit numbers, sums of those or,
+ * without a bias, of two scores.
  * Weights: w = scale * s_e of the chosen (the bias takes no part), divided by
  * their sum if renormalize.
  * An expert with a logit or a bias of -infinity or NaN is never chosen; a token
